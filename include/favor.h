@@ -267,6 +267,105 @@ int favor_decode_init(void* state, int B, int H, int d, int M, int feature_kind,
 int favor_decode_step(const void* q, const void* k, const void* v, const void* omega, void* state,
                       void* out, int B, int H, int d, int M, int feature_kind, void* stream);
 
+/*
+ * ---------------------------------------------------------------- linear attention with a decay
+ * Causal linear attention whose state forgets at one rate per head: with lambda = exp(log_decay[h]),
+ *   S_t = lambda S_{t-1} + k_t v_t^T,   out_t = S_t^T q_t,   S_{-1} = state_in (or zeros).
+ * The recurrence of the explainer's 核心机制 section (S_t = S_{t-1} + phi(k_t) v_t^T) with the
+ * identity feature map, a decay and no normaliser. q.k is taken as passed: any temperature is the
+ * caller's pre-scale of q and k (favor_rotary applies one).
+ *
+ * q, k, v, out: device, `dtype_code` 0 = float, 1 = bf16 (as favor_attention_host), [B, H, L, d].
+ *   strides: NULL (contiguous), or one favor_strides per operand in argument order, so that
+ *   token-major projections and slices of fused ones are read in place. d is contiguous. Inputs
+ *   may have stride 0 (a broadcast head); an output whose rows overlap returns FAVOR_ERR_SHAPE.
+ *   Base pointers are 16-byte aligned. Outputs must not overlap inputs; an output pointer equal to
+ *   an input's returns FAVOR_ERR_UNSUPPORTED.
+ * log_decay: device float [H], 4-byte aligned, natural logarithm of the decay: <= 0, -infinity
+ *   (lambda = 0: each token by itself) included. A positive value grows the state instead, and is
+ *   used as it is as long as exp(128 log_decay) is finite.
+ * lengths: device int [B] or NULL (every sequence has L tokens): tokens of each sequence, held to
+ *   [0, L]. Rows at and past the length are neither read into any result nor written. A sequence
+ *   of no tokens has state_out = state_in.
+ * state_in, state_out: device float [B, H, d, d] contiguous (row = k's column, column = v's), 16-byte
+ *   aligned, NULL = zeros / not wanted. state_out may be state_in (in place).
+ * Supported: 1 <= d <= 128, 1 <= L, dtype_code 0 or 1.
+ * Infinities and NaN reach what the recurrence takes them to, and nothing before them.
+ */
+typedef struct {
+  int64_t batch, head, token; /* element strides of a [B, H, L, d] operand */
+} favor_strides;
+
+/* The prompt form: chunks of tokens at a time. strides: q, k, v, out. */
+int favor_decay_attention(const void* q, const void* k, const void* v, const float* log_decay,
+                          const float* state_in, const int* lengths, void* out, float* state_out,
+                          int B, int H, int L, int d, int dtype_code, const favor_strides* strides,
+                          void* stream);
+
+/*
+ * Gradients of sum(dout . out) + sum(dstate_out . state_out), the same q, k, v, log_decay, state_in and
+ * lengths as the forward call's: with G_t = lambda G_{t+1} + q_t dout_t^T, started from dstate_out,
+ *   dq_t = S_t dout_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dstate_in = lambda G_0.
+ * The decay is a fixed slope per head and gets no gradient. dq, dk, dv: as out. dstate_out may be
+ * NULL (zeros), dstate_in may be NULL (not wanted) or dstate_out. strides: q, k, v, dout, dq, dk, dv.
+ * An input head shared through stride 0 gets one gradient per head; their sum is the caller's.
+ */
+int favor_decay_attention_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                                   const float* state_in, const int* lengths, const void* dout,
+                                   const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in,
+                                   int B, int H, int L, int d, int dtype_code, const favor_strides* strides,
+                                   void* stream);
+
+/*
+ * One token per (batch, head) against the carried state, which is updated in place. q, k, v, out
+ * [B, H, d]; strides: q, k, v, out (token unused). state [B, H, d, d] as above: calls on one state must
+ * be ordered. Calls on tokens t, t + 1, ... continue favor_decay_attention's state_out.
+ */
+int favor_decay_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                     void* out, int B, int H, int d, int dtype_code, const favor_strides* strides,
+                     void* stream);
+
+/* Bytes of scratch one favor_decay_attention (backward != 0: _backward) call on contiguous operands
+ * takes from the library's stream-ordered pool (host only). 0 for sizes it does not take. */
+size_t favor_decay_workspace_bytes(int B, int H, int L, int d, int dtype_code, int backward);
+
+/*
+ * Rotary positions of q [B, Hq, L, d] and k [B, Hk, L, d] in one launch, with the caller's pre-scale of
+ * both (d^-1/4 for favor_attention). The first `rot` columns are rot/2 pairs: columns (2i, 2i+1)
+ * where interleaved != 0, else (i, i + rot/2). Pair i of a token at position t turns by t freq[i]:
+ *   (x1, x2) -> scale rot_scale (x1 cos - x2 sin, x1 sin + x2 cos);
+ * the other columns are multiplied by `scale`. inverse != 0 turns the other way: the gradient (the
+ * transposed map, with the same scales).
+ * freq: device double [rot/2], radians per position (favor_rotary_frequencies). positions: device int
+ * [B, L], or NULL for first_position + t. Angles are reduced in double, so far positions keep their
+ * accuracy. k, k_out: NULL with Hk = 0. q_out may be q and k_out may be k with the same strides (in
+ * place). strides: q, k, q_out, k_out (NULL = contiguous). Data pointers are 16-byte aligned, freq
+ * 8-byte, positions 4-byte. Supported: rot even, 2 <= rot <= d <= 65536, Hq + Hk <= 65535.
+ */
+int favor_rotary(const void* q, const void* k, const double* freq, const int* positions, void* q_out,
+                 void* k_out, int B, int Hq, int Hk, int L, int d, int rot, int interleaved, int inverse,
+                 int first_position, float scale, float rot_scale, int dtype_code,
+                 const favor_strides* strides, void* stream);
+
+/*
+ * Rotary frequencies (host only: freq is host memory of rot/2 doubles, rot_scale one double):
+ *   FAVOR_ROTARY_PLAIN   base^(-2i/rot)
+ *   FAVOR_ROTARY_LINEAR  the same divided by `factor` (positions interpolated)
+ *   FAVOR_ROTARY_BASE    base raised to base factor^(rot/(rot-2)): the slowest pair is interpolated by
+ *                        factor, the fastest kept
+ *   FAVOR_ROTARY_PARTS   by wavelength: pairs that turn at least beta_fast times over trained_length are
+ *                        kept, at most beta_slow times interpolated by factor, a linear ramp between;
+ *                        *rot_scale = 0.1 ln(factor) + 1 (elsewhere 1), to pass to favor_rotary
+ */
+typedef enum {
+  FAVOR_ROTARY_PLAIN = 0,
+  FAVOR_ROTARY_LINEAR = 1,
+  FAVOR_ROTARY_BASE = 2,
+  FAVOR_ROTARY_PARTS = 3
+} favor_rotary_scaling;
+int favor_rotary_frequencies(double* freq, double* rot_scale, int rot, double base, int scaling, double factor,
+                             double trained_length, double beta_fast, double beta_slow);
+
 /* Synchronise `stream`, then read and clear the device status word (FAVOR_OK or a code). */
 int favor_sync_status(void* stream);
 

@@ -10,7 +10,9 @@ Entry points mirror the C ABI in include/favor.h:
     favor_selftest_timeout, favor_selftest_sincos, favor_attention_f32_noalloc,
     favor_noalloc_scratch_bytes,
     favor_decode_state_bytes, favor_decode_init, favor_decode_step, favor_orf_omega_seeded,
-    favor_orf_gaussians_seeded, favor_philox4x64, favor_attention_backward_f32
+    favor_orf_gaussians_seeded, favor_philox4x64, favor_attention_backward_f32,
+    favor_decay_attention, favor_decay_attention_backward, favor_decay_step,
+    favor_decay_workspace_bytes, favor_rotary, favor_rotary_frequencies
 """
 from __future__ import annotations
 
@@ -19,6 +21,7 @@ import os
 
 FAVOR_TRIG = 0
 FAVOR_RELU = 1
+FAVOR_ROTARY_PLAIN, FAVOR_ROTARY_LINEAR, FAVOR_ROTARY_BASE, FAVOR_ROTARY_PARTS = 0, 1, 2, 3
 STATUS = {
     0: "FAVOR_OK", -1: "FAVOR_ERR_NULL", -2: "FAVOR_ERR_ALIGN", -3: "FAVOR_ERR_SHAPE",
     -4: "FAVOR_ERR_KIND", -5: "FAVOR_ERR_UNSUPPORTED", -6: "FAVOR_ERR_CUDA",
@@ -27,6 +30,7 @@ STATUS = {
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfavor.so")
 
 _vp, _i, _ll, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_uint64
+_f, _d = ctypes.c_float, ctypes.c_double
 _SIGS = {
     "favor_attention": (_i, [_vp] * 5 + [_i] * 7 + [_vp]),
     "favor_attention_chunked": (_i, [_vp] * 5 + [_i] * 8 + [_vp]),
@@ -47,6 +51,12 @@ _SIGS = {
     "favor_orf_gaussians_seeded": (_i, [_u64, _vp, _vp] + [_i] * 3 + [_vp]),
     "favor_philox4x64": (_i, [_u64, _u64, _u64, _vp, _vp]),
     "favor_attention_backward_f32": (_i, [_vp] * 8 + [_i] * 7 + [_vp]),
+    "favor_decay_attention": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _vp]),
+    "favor_decay_attention_backward": (_i, [_vp] * 12 + [_i] * 5 + [_vp, _vp]),
+    "favor_decay_step": (_i, [_vp] * 6 + [_i] * 4 + [_vp, _vp]),
+    "favor_decay_workspace_bytes": (_sz, [_i] * 6),
+    "favor_rotary": (_i, [_vp] * 6 + [_i] * 9 + [_f, _f, _i, _vp, _vp]),
+    "favor_rotary_frequencies": (_i, [_vp, _vp, _i, _d, _i] + [_d] * 4),
 }
 _LIB = None
 
@@ -364,3 +374,234 @@ def favor_attention_backward_f32(q, k, v, omega, dout, feature_kind=FAVOR_TRIG, 
                                             B, H, L, d, M, int(feature_kind), int(causal), _stream(stream))
     _check(rc, "favor_attention_backward_f32")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- linear attention with a decay
+def _rows(name, t, shape, dtype, device):
+    """An operand [B, H, L, d] (or [B, H, d]) read in place: any strides, d contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _aux(name, t, shape, dtype, device):
+    """A contiguous companion tensor (decays, lengths, states, positions), or None."""
+    import torch
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _strides(*ts):
+    """favor_strides of the operands, or None where all are contiguous."""
+    if all(t is None or t.is_contiguous() for t in ts):
+        return None
+    a = []
+    for t in ts:
+        a += [0, 0, 0] if t is None else [*t.stride()[:-1], 0][:3]
+    return (_ll * len(a))(*a)
+
+
+def _first(name, t, dims):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have shape {'[B, H, L, d]' if dims == 4 else '[B, H, d]'}")
+    return 0 if t.dtype == torch.float32 else 1
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream it launches on: the given one (a
+    stream or its handle), else that device's current one. Tensors made inside belong to that stream."""
+
+    __slots__ = ("ctx", "handle")
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = []
+        if torch.cuda.current_device() != device.index:
+            self.ctx.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.ctx.append(torch.cuda.stream(stream))
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None, state_out=None,
+                          return_state=False, stream=None):
+    """Causal linear attention with a decay per head: S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
+    out_t = S_t^T q_t (favor_decay_attention in include/favor.h). q, k, v: [B, H, L, d] bf16 or float32,
+    any strides with d contiguous; log_decay: float32 [H]; state: float32 [B, H, d, d] carried in, or
+    None; lengths: int32 [B] or None. Returns out, or (out, state_out) where return_state is true or
+    state_out is given. Rows past a sequence's length are left as they were in a given `out`, and zero
+    in a new one. state_out may be `state`."""
+    import torch
+    code = _first("q", q, 4)
+    B, H, L, d = q.shape
+    dev = q.device
+    _rows("k", k, q.shape, q.dtype, dev)
+    _rows("v", v, q.shape, q.dtype, dev)
+    _rows("q", q, q.shape, q.dtype, dev)
+    if log_decay is None:
+        raise TypeError("log_decay must be a float32 tensor")
+    g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
+    s_in = _aux("state", state, (B, H, d, d), torch.float32, dev)
+    n = _aux("lengths", lengths, (B,), torch.int32, dev)
+    with _On(dev, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            if lengths is not None:
+                out.zero_()
+        _rows("out", out, q.shape, q.dtype, dev)
+        if state_out is None and return_state:
+            state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+        s_out = _aux("state_out", state_out, (B, H, d, d), torch.float32, dev)
+        rc = lib().favor_decay_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), g, s_in, n, out.data_ptr(), s_out,
+                                         B, H, L, d, code, _strides(q, k, v, out), handle)
+    _check(rc, "favor_decay_attention")
+    return out if state_out is None else (out, state_out)
+
+
+def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=None, lengths=None, dq=None, dk=None,
+                                   dv=None, dstate_in=None, stream=None):
+    """Gradients (dq, dk, dv) of sum(dout * out) + sum(dstate * state_out) for the outputs of
+    favor_decay_attention on the same arguments; with `state`, `dstate` or `dstate_in` given, (dq, dk, dv,
+    dstate_in). dstate: float32 [B, H, d, d] or None (zeros). Rows past a sequence's length are left
+    as they were in given outputs, and zero in new ones. log_decay gets no gradient."""
+    import torch
+    code = _first("q", q, 4)
+    B, H, L, d = q.shape
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v), ("dout", dout)):
+        _rows(name, t, q.shape, q.dtype, dev)
+    if log_decay is None:
+        raise TypeError("log_decay must be a float32 tensor")
+    g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
+    s_in = _aux("state", state, (B, H, d, d), torch.float32, dev)
+    ds = _aux("dstate", dstate, (B, H, d, d), torch.float32, dev)
+    n = _aux("lengths", lengths, (B,), torch.int32, dev)
+    with _On(dev, stream) as handle:
+        outs = []
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            if t is None:
+                t = torch.empty_like(q, memory_format=torch.contiguous_format)
+                if lengths is not None:
+                    t.zero_()
+            _rows(name, t, q.shape, q.dtype, dev)
+            outs.append(t)
+        dq, dk, dv = outs
+        if dstate_in is None and (state is not None or dstate is not None):
+            dstate_in = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+        ds_in = _aux("dstate_in", dstate_in, (B, H, d, d), torch.float32, dev)
+        rc = lib().favor_decay_attention_backward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g, s_in, n, dout.data_ptr(), ds, dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), ds_in, B, H, L, d, code, _strides(q, k, v, dout, dq, dk, dv), handle)
+    _check(rc, "favor_decay_attention_backward")
+    return (dq, dk, dv) if dstate_in is None else (dq, dk, dv, dstate_in)
+
+
+def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
+    """One token per head against the carried state, updated in place: S = exp(log_decay[h]) S + k v^T,
+    out = S^T q. q, k, v: [B, H, d] bf16 or float32 (slices of fused projections are read in place);
+    state: float32 [B, H, d, d]. Returns out [B, H, d]."""
+    import torch
+    code = _first("q", q, 3)
+    B, H, d = q.shape
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _rows(name, t, q.shape, q.dtype, dev)
+    if log_decay is None or state is None:
+        raise TypeError("log_decay and state must be float32 tensors")
+    g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
+    s = _aux("state", state, (B, H, d, d), torch.float32, dev)
+    with _On(dev, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _rows("out", out, q.shape, q.dtype, dev)
+        rc = lib().favor_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g, s, out.data_ptr(), B, H, d, code,
+                                    _strides(q, k, v, out), handle)
+    _check(rc, "favor_decay_step")
+    return out
+
+
+def favor_decay_workspace_bytes(B, H, L, d, dtype_code=1, backward=False) -> int:
+    return lib().favor_decay_workspace_bytes(B, H, L, d, int(dtype_code), int(backward))
+
+
+# ---------------------------------------------------------------- rotary positions
+def favor_rotary_frequencies(rot, base=10000.0, scaling=FAVOR_ROTARY_PLAIN, factor=1.0, trained_length=0,
+                             beta_fast=32.0, beta_slow=1.0, device=None):
+    """(freq, rot_scale): float64 [rot/2] radians per position, on `device` (CPU if None), and the scale of
+    the rotated columns to pass to favor_rotary. Scalings: favor_rotary_frequencies in include/favor.h."""
+    import torch
+    freq = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    rs = ctypes.c_double(1.0)
+    rc = lib().favor_rotary_frequencies(freq.data_ptr(), ctypes.addressof(rs), int(rot), float(base), int(scaling),
+                                        float(factor), float(trained_length), float(beta_fast), float(beta_slow))
+    _check(rc, "favor_rotary_frequencies")
+    return (freq if device is None else freq.to(device)), rs.value
+
+
+def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False, inverse=False, scale=1.0,
+                 rot_scale=1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [B, Hq, L, d] and k [B, Hk, L, d] (or None) in one launch: the first
+    2 len(freq) columns turn by positions * freq, all are multiplied by `scale`, the rotated ones by
+    rot_scale too. freq: float64 [rot/2]; positions: int32 [B, L], or None for first_position + t.
+    inverse=True is the gradient of the same call. q_out / k_out may be q / k (in place). Returns
+    (q_out, k_out)."""
+    import torch
+    code = _first("q", q, 4)
+    B, Hq, L, d = q.shape
+    dev = q.device
+    _rows("q", q, q.shape, q.dtype, dev)
+    Hk = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise TypeError("k must be a CUDA tensor of shape [B, Hk, L, d]")
+        Hk = k.shape[1]
+        _rows("k", k, (B, Hk, L, d), q.dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if freq is None or freq.dim() != 1:
+        raise TypeError("freq must be a float64 tensor of shape [rot/2]")
+    f = _aux("freq", freq, freq.shape, torch.float64, dev)
+    pos = _aux("positions", positions, (B, L), torch.int32, dev)
+    with _On(dev, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _rows("q_out", q_out, q.shape, q.dtype, dev)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            _rows("k_out", k_out, k.shape, q.dtype, dev)
+        rc = lib().favor_rotary(q.data_ptr(), None if k is None else k.data_ptr(), f, pos, q_out.data_ptr(),
+                                None if k is None else k_out.data_ptr(), B, Hq, Hk, L, d, 2 * freq.numel(),
+                                int(interleaved), int(inverse), int(first_position), scale, rot_scale, code,
+                                _strides(q, k, q_out, k_out), handle)
+    _check(rc, "favor_rotary")
+    return q_out, k_out

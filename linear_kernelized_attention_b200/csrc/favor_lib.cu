@@ -9,6 +9,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/favor.h"
@@ -992,3 +993,5 @@ int favor_selftest_sincos(const float* u, float* sin_out, float* cos_out, int n,
 }
 
 }  // extern "C"
+
+#include "host_decay.cuh"

@@ -1,0 +1,127 @@
+"""Host checks of the decayed linear attention and rotary entry points: bad arguments are refused before any
+CUDA call (the pointers are made up and never read)."""
+import ctypes
+
+import pytest
+
+import linear_kernelized_attention_b200 as F
+
+vp = ctypes.c_void_p
+
+
+def _strides(rows):
+    flat = [x for r in rows for x in r]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def _attend(**o):
+    a = dict(q=16, k=32, v=48, g=64, s_in=0, n=0, out=80, s_out=0, B=2, H=2, L=8, d=64, dt=1, st=None)
+    a.update(o)
+    return F.lib().favor_decay_attention(vp(a["q"]), vp(a["k"]), vp(a["v"]), vp(a["g"]), vp(a["s_in"]), vp(a["n"]),
+                                         vp(a["out"]), vp(a["s_out"]), a["B"], a["H"], a["L"], a["d"], a["dt"],
+                                         a["st"], None)
+
+
+OK = (1024, 512, 64)
+COMMON = [
+    ({"q": 0}, -1), ({"k": 0}, -1), ({"v": 0}, -1), ({"g": 0}, -1),
+    ({"k": 34}, -2), ({"g": 66}, -2),
+    ({"B": 0}, -3), ({"H": -1}, -3), ({"d": 0}, -3), ({"B": 1 << 20, "H": 1 << 20}, -3),
+    ({"d": 129}, -5), ({"dt": 2}, -5), ({"dt": -1}, -5),
+]
+
+
+@pytest.mark.parametrize("over,code", COMMON + [
+    ({"out": 0}, -1), ({"s_in": 20}, -2), ({"s_out": 8}, -2), ({"n": 3}, -2), ({"out": 16}, -5), ({"out": 48}, -5),
+    ({"L": 0}, -3),
+    ({"st": [OK, OK, OK, (1024, 512, 32)]}, -3),     # rows of the output overlap
+    ({"st": [OK, OK, OK, (1024, 0, 64)]}, -3),       # heads of the output overlap
+    ({"st": [OK, OK, OK, (512, 512, 64)]}, -3),
+    ({"st": [OK, (-1024, 512, 64), OK, OK]}, -3),
+    ({"st": [OK, OK, (1 << 43, 512, 64), OK]}, -3),
+])
+def test_attention_refuses(over, code):
+    if isinstance(over.get("st"), list):
+        over = dict(over, st=_strides(over["st"]))
+    assert _attend(**over) == code
+
+
+def _backward(**o):
+    a = dict(q=16, k=32, v=48, g=64, s_in=0, n=0, do=80, ds=0, dq=96, dk=112, dv=128, ds_in=0, B=2, H=2, L=8, d=64,
+             dt=1, st=None)
+    a.update(o)
+    return F.lib().favor_decay_attention_backward(
+        vp(a["q"]), vp(a["k"]), vp(a["v"]), vp(a["g"]), vp(a["s_in"]), vp(a["n"]), vp(a["do"]), vp(a["ds"]),
+        vp(a["dq"]), vp(a["dk"]), vp(a["dv"]), vp(a["ds_in"]), a["B"], a["H"], a["L"], a["d"], a["dt"], a["st"], None)
+
+
+@pytest.mark.parametrize("over,code", COMMON + [
+    ({"do": 0}, -1), ({"dq": 0}, -1), ({"dk": 0}, -1), ({"dv": 0}, -1), ({"ds": 4}, -2), ({"ds_in": 24}, -2),
+    ({"L": 0}, -3), ({"dq": 16}, -5), ({"dk": 96}, -5), ({"dv": 112}, -5), ({"dv": 80}, -5),
+    ({"st": [OK] * 6 + [(1024, 512, 0)]}, -3), ({"st": [OK] * 4 + [(0, 512, 64)] + [OK] * 2}, -3),
+])
+def test_backward_refuses(over, code):
+    if isinstance(over.get("st"), list):
+        over = dict(over, st=_strides(over["st"]))
+    assert _backward(**over) == code
+
+
+def _step(**o):
+    a = dict(q=16, k=32, v=48, g=64, s=80, out=96, B=2, H=2, d=64, dt=1, st=None)
+    a.update(o)
+    return F.lib().favor_decay_step(vp(a["q"]), vp(a["k"]), vp(a["v"]), vp(a["g"]), vp(a["s"]), vp(a["out"]), a["B"],
+                                    a["H"], a["d"], a["dt"], a["st"], None)
+
+
+@pytest.mark.parametrize("over,code", COMMON + [
+    ({"s": 0}, -1), ({"out": 0}, -1), ({"s": 84}, -2), ({"out": 16}, -5),
+    ({"st": [OK, OK, OK, (64, 64, 0)]}, -3),
+])
+def test_step_refuses(over, code):
+    if isinstance(over.get("st"), list):
+        over = dict(over, st=_strides(over["st"]))
+    assert _step(**over) == code
+
+
+def _rotary(**o):
+    a = dict(q=16, k=32, f=64, n=0, qo=80, ko=96, B=2, Hq=2, Hk=1, L=8, d=64, rot=32, dt=1, st=None)
+    a.update(o)
+    return F.lib().favor_rotary(vp(a["q"]), vp(a["k"]), vp(a["f"]), vp(a["n"]), vp(a["qo"]), vp(a["ko"]), a["B"],
+                                a["Hq"], a["Hk"], a["L"], a["d"], a["rot"], 0, 0, 0, 1.0, 1.0, a["dt"], a["st"], None)
+
+
+@pytest.mark.parametrize("over,code", [
+    ({"q": 0}, -1), ({"k": 0}, -1), ({"f": 0}, -1), ({"qo": 0}, -1), ({"ko": 0}, -1),
+    ({"q": 18}, -2), ({"ko": 97}, -2), ({"f": 68}, -2), ({"n": 6}, -2),
+    ({"B": 0}, -3), ({"Hq": 0}, -3), ({"Hk": -1}, -3), ({"L": -2}, -3), ({"rot": 0}, -3), ({"rot": 7}, -3),
+    ({"rot": 66}, -3), ({"dt": 3}, -5), ({"Hq": 65535}, -5),
+    ({"qo": 32}, -5), ({"ko": 16}, -5), ({"ko": 80}, -5),
+    ({"st": [OK, OK, (1024, 512, 0), OK]}, -3),
+    ({"qo": 16, "st": [OK, OK, (2048, 1024, 128), OK]}, -5),  # in place with other strides
+])
+def test_rotary_refuses(over, code):
+    if isinstance(over.get("st"), list):
+        over = dict(over, st=_strides(over["st"]))
+    assert _rotary(**over) == code
+
+
+def test_workspace_is_host_only():
+    assert F.favor_decay_workspace_bytes(1, 1, 0, 64) == 0
+    assert F.favor_decay_workspace_bytes(1, 1, 8, 129) == 0
+    assert F.favor_decay_workspace_bytes(1, 1, 8, 64, 2) == 0
+    assert F.favor_decay_workspace_bytes(2, 3, 1000, 40, 0) > 0
+    assert F.favor_decay_workspace_bytes(2, 3, 1000, 40, 0, True) >= F.favor_decay_workspace_bytes(2, 3, 1000, 40, 0)
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    x = torch.zeros(1, 1, 4, 8)
+    g = torch.zeros(1)
+    with pytest.raises(TypeError):
+        F.favor_decay_attention(x, x, x, g)
+    with pytest.raises(TypeError):
+        F.favor_decay_attention_backward(x, x, x, g, x)
+    with pytest.raises(TypeError):
+        F.favor_decay_step(x[:, :, 0], x[:, :, 0], x[:, :, 0], g, torch.zeros(1, 1, 8, 8))
+    with pytest.raises(TypeError):
+        F.favor_rotary(x, x, torch.zeros(4, dtype=torch.float64))

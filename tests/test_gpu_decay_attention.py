@@ -1,0 +1,374 @@
+"""Decayed linear attention on the GPU (prompts and gradients) against the float64 recurrence; tolerances in
+decay_cases."""
+import numpy as np
+import pytest
+
+import decay_cases as C
+from oracle import decay_oracle as D
+
+pytestmark = pytest.mark.gpu
+
+# one token, chunk borders (64 and 128 tokens), segments, odd head sizes, every route
+SHAPES = [
+    (1, 1, 1, 1), (2, 3, 1, 64), (1, 2, 2, 128), (2, 2, 63, 16), (1, 2, 64, 64), (1, 3, 65, 32), (2, 2, 127, 64),
+    (1, 2, 128, 128), (1, 2, 129, 64), (1, 3, 200, 48), (1, 2, 257, 100), (2, 2, 300, 17), (1, 2, 385, 80),
+    (1, 2, 640, 128), (3, 2, 1023, 64), (1, 1, 2049, 64), (1, 2, 1500, 8),
+]
+
+
+def _dtype(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def _inputs(B, H, L, d, dtype, seed, n=3):
+    s = d ** -0.25
+    return [C.draw((B, H, L, d), seed + i, dtype, s if i < 2 else 1.0) for i in range(n)]
+
+
+def _state(B, H, d, seed):
+    import torch
+    return C.draw((B, H, d, d), seed, torch.float32)
+
+
+def _forward_case(B, H, L, d, name, state, lengths=None, rows="bhld", g=None, seed=0):
+    import torch
+    import linear_kernelized_attention_b200 as F
+    dt = _dtype(name)
+    (q, qn), (k, kn), (v, vn) = _inputs(B, H, L, d, dt, seed + 10)
+    g = C.slopes(H, seed + L) if g is None else np.asarray(g, dtype=np.float32)
+    S, Sn = _state(B, H, d, seed + 90) if state else (None, None)
+    ref, refS = D.decay_attention(qn, kn, vn, g, Sn, lengths)
+    mag, magS = D.decay_attention(abs(qn), abs(kn), abs(vn), g, None if Sn is None else abs(Sn), lengths)
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out = torch.full((B, H, L, d), 7.0, dtype=dt, device="cuda")
+    got, gotS = F.favor_decay_attention(*(C.place(x, rows) for x in (q, k, v)), torch.from_numpy(g).cuda(),
+                                        state=None if S is None else S.cuda(), lengths=n, out=out, return_state=True)
+    assert F.favor_sync_status() == 0
+    what = f"{B}x{H}x{L} d={d} {name} {rows} state={state} lengths={lengths}"
+    assert got is out
+    if lengths is not None:
+        for b, m in enumerate(np.clip(lengths, 0, L)):
+            assert bool((out[b, :, m:] == 7.0).all()), f"{what}: rows past the length were written"
+            out[b, :, m:] = 0.0
+    w = C.check(got, ref, mag, d, L, name == "bf16", what, f32_operands=name == "f32")
+    ws = C.check(gotS, refS, magS, d, L, False, what + " state", f32_operands=name == "f32")
+    print(what, f"{w:.3f} {ws:.3f}")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,L,d", SHAPES)
+def test_forward(B, H, L, d, name):
+    _forward_case(B, H, L, d, name, state=(L + d) % 2 == 0)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", ["blhd", "fused"])
+@pytest.mark.parametrize("B,H,L,d", [(2, 3, 200, 64), (1, 2, 130, 128), (2, 2, 70, 24)])
+def test_forward_strides(B, H, L, d, rows, name):
+    _forward_case(B, H, L, d, name, state=True, rows=rows)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("L,d,lengths", [
+    (300, 64, [0, 1, 300, 128, 129]), (129, 128, [127, 128, 129, 64, 0]), (700, 32, [700, 65, 513, 1, 699]),
+    (50, 64, [-3, 60, 50, 49, 2]),  # held to [0, L]
+])
+def test_forward_lengths(L, d, lengths, name):
+    _forward_case(5, 2, L, d, name, state=True, lengths=lengths, rows="blhd")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("g", [0.0, -np.inf, -100.0, -1e-6, 0.01])
+def test_forward_decays(g, name):
+    _forward_case(1, 1, 400, 64, name, state=True, g=[g])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_many_heads(name):
+    """More heads than SMs: no segments."""
+    _forward_case(20, 10, 150, 64, name, state=True)
+
+
+def test_long_sequence_many_segments():
+    _forward_case(1, 1, 9000, 64, "bf16", state=True, g=[-1e-3])
+
+
+def _backward_case(B, H, L, d, name, state, lengths=None, rows="bhld", g=None, seed=0):
+    import torch
+    import linear_kernelized_attention_b200 as F
+    dt = _dtype(name)
+    (q, qn), (k, kn), (v, vn), (do, don) = _inputs(B, H, L, d, dt, seed + 40, 4)
+    g = C.slopes(H, seed + L) if g is None else np.asarray(g, dtype=np.float32)
+    S, Sn = _state(B, H, d, seed + 91) if state else (None, None)
+    dS, dSn = _state(B, H, d, seed + 92) if state else (None, None)
+    ref = D.decay_backward(qn, kn, vn, g, don, Sn, dSn, lengths)
+    mag = D.decay_backward(abs(qn), abs(kn), abs(vn), g, abs(don), None if Sn is None else abs(Sn),
+                           None if dSn is None else abs(dSn), lengths)
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    outs = [torch.full((B, H, L, d), 7.0, dtype=dt, device="cuda") for _ in range(3)]
+    dsi = torch.empty(B, H, d, d, device="cuda")
+    got = F.favor_decay_attention_backward(
+        *(C.place(x, rows) for x in (q, k, v)), torch.from_numpy(g).cuda(), C.place(do, rows),
+        state=None if S is None else S.cuda(), dstate=None if dS is None else dS.cuda(), lengths=n, dq=outs[0],
+        dk=outs[1], dv=outs[2], dstate_in=dsi)
+    assert F.favor_sync_status() == 0
+    what = f"{B}x{H}x{L} d={d} {name} {rows} state={state} lengths={lengths}"
+    worst = []
+    for i, part in enumerate(("dq", "dk", "dv")):
+        if lengths is not None:
+            for b, m in enumerate(np.clip(lengths, 0, L)):
+                assert bool((outs[i][b, :, m:] == 7.0).all()), f"{what}: {part} rows past the length were written"
+                outs[i][b, :, m:] = 0.0
+        worst.append(C.check(got[i], ref[i], mag[i], d, L, name == "bf16", f"{what} {part}", name == "f32"))
+    worst.append(C.check(got[3], ref[3], mag[3], d, L, False, f"{what} dstate_in", name == "f32"))
+    print(what, " ".join(f"{x:.3f}" for x in worst))
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,L,d", SHAPES)
+def test_backward(B, H, L, d, name):
+    _backward_case(B, H, L, d, name, state=(L + d) % 2 == 1)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", ["blhd", "fused"])
+@pytest.mark.parametrize("B,H,L,d", [(2, 3, 200, 64), (1, 2, 130, 128), (2, 2, 70, 24)])
+def test_backward_strides(B, H, L, d, rows, name):
+    _backward_case(B, H, L, d, name, state=True, rows=rows)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("L,d,lengths", [
+    (300, 64, [0, 1, 300, 128, 129]), (129, 128, [127, 128, 129, 64, 0]), (700, 32, [700, 65, 513, 1, 699]),
+])
+def test_backward_lengths(L, d, lengths, name):
+    _backward_case(5, 2, L, d, name, state=True, lengths=lengths, rows="blhd")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("g", [0.0, -np.inf, -100.0, -1e-6])
+def test_backward_decays(g, name):
+    _backward_case(1, 1, 400, 64, name, state=True, g=[g])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_backward_many_heads(name):
+    _backward_case(20, 10, 150, 64, name, state=True)
+
+
+def test_backward_long_sequence():
+    _backward_case(1, 1, 5000, 64, "bf16", state=True, g=[-1e-3])
+
+
+# ------------------------------------------------------------------ beyond values
+def _simple(B=2, H=3, L=260, d=64, name="bf16", seed=5):
+    import torch
+    dt = _dtype(name)
+    q, k, v, do = (x[0].cuda() for x in _inputs(B, H, L, d, dt, seed, 4))
+    return q, k, v, do, torch.from_numpy(C.slopes(H)).cuda()
+
+
+@pytest.mark.parametrize("name,d", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 20)])
+@pytest.mark.parametrize("where", ["v", "k", "q"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_later_non_finite_tokens_do_not_reach_earlier_rows(name, d, where, bad):
+    """A NaN or an infinity in token t of q reaches row t alone, in k or v the rows from t on."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, _, g = _simple(1, 2, 300, d, name)
+    clean = F.favor_decay_attention(q, k, v, g)
+    x = dict(q=q.clone(), k=k.clone(), v=v.clone())
+    for t, c in ((77, 3), (200, d - 1)):
+        x[where][0, 0, t, c] = float(bad)
+    got = F.favor_decay_attention(x["q"], x["k"], x["v"], g)
+    assert torch.equal(got[0, 1], clean[0, 1])
+    if where == "q":
+        keep = [t for t in range(300) if t not in (77, 200)]
+        assert torch.equal(got[0, 0, keep], clean[0, 0, keep])
+        assert not torch.isfinite(got[0, 0, 77]).any()
+        return
+    assert torch.equal(got[0, 0, :77], clean[0, 0, :77])
+    if where == "v":  # only the token's column
+        assert not torch.isfinite(got[0, 0, 77:, 3]).any()
+        assert not torch.isfinite(got[0, 0, 200:, d - 1]).any()
+        assert torch.equal(got[0, 0, 77:200, d - 1], clean[0, 0, 77:200, d - 1])
+        cols = [c for c in range(d) if c not in (3, d - 1)]
+        assert torch.equal(got[0, 0][:, cols], clean[0, 0][:, cols])
+    else:
+        assert not torch.isfinite(got[0, 0, 77:]).any()
+
+
+@pytest.mark.parametrize("name,d", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 20)])
+def test_tokens_past_the_length_are_never_read_into_results(name, d):
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(3, 2, 270, d, name)
+    n = torch.tensor([140, 0, 129], dtype=torch.int32, device="cuda")
+    clean = F.favor_decay_attention(q, k, v, g, lengths=n, return_state=True)
+    cgrad = F.favor_decay_attention_backward(q, k, v, g, do, lengths=n)
+    for b, m in enumerate((140, 0, 129)):
+        for t in (q, k, v, do):
+            t[b, :, m:] = float("nan")
+    got = F.favor_decay_attention(q, k, v, g, lengths=n, return_state=True)
+    ggrad = F.favor_decay_attention_backward(q, k, v, g, do, lengths=n)
+    for a, b in zip((*clean, *cgrad), (*got, *ggrad)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name,d,where", [("f32", 64, "do"), ("bf16", 64, "do"), ("bf16", 128, "q"), ("bf16", 64, "k")])
+def test_gradients_keep_non_finite_tokens_to_their_rows(name, d, where):
+    """A NaN in token t: of dout or q it reaches dk, dv of rows up to t; of k it reaches dq from t on."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(1, 1, 300, d, name)
+    clean = F.favor_decay_attention_backward(q, k, v, g, do)
+    t = 150
+    {"q": q, "k": k, "do": do}[where][0, 0, t, 2] = float("nan")
+    dq, dk, dv = F.favor_decay_attention_backward(q, k, v, g, do)
+    if where == "k":
+        assert torch.equal(dq[:, :, :t], clean[0][:, :, :t]) and torch.equal(dk, clean[1])
+        others = [i for i in range(300) if i != t]
+        assert torch.equal(dv[:, :, others], clean[2][:, :, others])
+    else:
+        assert torch.equal(dk[:, :, t + 1:], clean[1][:, :, t + 1:])
+        assert torch.equal(dv[:, :, t + 1:], clean[2][:, :, t + 1:])
+        if where == "do":
+            others = [i for i in range(300) if i != t]
+            assert torch.equal(dq[:, :, others], clean[0][:, :, others])
+        else:
+            assert torch.equal(dq, clean[0])
+
+
+@pytest.mark.parametrize("name,L", [("bf16", 64), ("bf16", 2000), ("f32", 500)])
+def test_state_in_place_and_split_prompt(name, L):
+    """state_out = state_in's tensor; two calls carry the state; equal to one call within the tolerance of the
+    operands' rounding (the cut moves the chunk borders)."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, _, g = _simple(1, 2, L, 64, name)
+    S0 = torch.randn(1, 2, 64, 64, device="cuda")
+    _, ref = F.favor_decay_attention(q, k, v, g, state=S0, return_state=True)
+    S = S0.clone()
+    out, same = F.favor_decay_attention(q, k, v, g, state=S, state_out=S)
+    assert same is S and torch.equal(S, ref)
+    m = L // 3
+    S = S0.clone()
+    F.favor_decay_attention(q[:, :, :m], k[:, :, :m], v[:, :, :m], g, state=S, state_out=S)
+    F.favor_decay_attention(q[:, :, m:], k[:, :, m:], v[:, :, m:], g, state=S, state_out=S)
+    assert float((S - ref).norm() / ref.norm()) < 2.0 ** -16
+
+
+def test_repeated_calls_are_identical():
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(2, 4, 1100, 64)
+    a = (*F.favor_decay_attention(q, k, v, g, return_state=True), *F.favor_decay_attention_backward(q, k, v, g, do))
+    for _ in range(3):
+        b = (*F.favor_decay_attention(q, k, v, g, return_state=True), *F.favor_decay_attention_backward(q, k, v, g, do))
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+def test_broadcast_head(name):
+    """One k and v head shared by every query head through stride 0."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(2, 3, 200, 64, name)
+    k1, v1 = k[:, :1].expand_as(q), v[:, :1].expand_as(q)
+    got = F.favor_decay_attention(q, k1, v1, g)
+    ref = F.favor_decay_attention(q, k1.contiguous(), v1.contiguous(), g)
+    tol = 2.0 ** -7 if name == "bf16" else 2.0 ** -16
+    assert float((got.float() - ref.float()).norm()) <= tol * float(ref.float().norm())
+    got = F.favor_decay_attention_backward(q, k1, v1, g, do)
+    ref = F.favor_decay_attention_backward(q, k1.contiguous(), v1.contiguous(), g, do)
+    for a, b in zip(got, ref):
+        assert float((a.float() - b.float()).norm()) <= tol * float(b.float().norm())
+
+
+def test_graph_capture_and_replay():
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(1, 3, 900, 64)
+    S = torch.zeros(1, 3, 64, 64, device="cuda")
+    F.favor_decay_attention(q, k, v, g, state=S, return_state=True)
+    F.favor_decay_attention_backward(q, k, v, g, do)
+    out, so = torch.empty_like(q), torch.empty_like(S)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        F.favor_decay_attention(q, k, v, g, state=S, out=out, state_out=so)
+    with torch.cuda.graph(g2):
+        F.favor_decay_attention_backward(q, k, v, g, do, dq=grads[0], dk=grads[1], dv=grads[2])
+    for seed in (21, 22):
+        fresh = _simple(1, 3, 900, 64, seed=seed)
+        for a, b in zip((q, k, v, do), fresh):
+            a.copy_(b)
+        S.normal_()
+        g2.replay()
+        g1.replay()
+        ref = F.favor_decay_attention(q, k, v, g, state=S, return_state=True)
+        rg = F.favor_decay_attention_backward(q, k, v, g, do)
+        assert torch.equal(out, ref[0]) and torch.equal(so, ref[1])
+        assert all(torch.equal(a, b) for a, b in zip(grads, rg))
+
+
+def test_two_streams_at_once():
+    import torch
+    import linear_kernelized_attention_b200 as F
+    sets = [_simple(2, 4, 700, 64, seed=s) for s in (31, 32)]
+    refs = [F.favor_decay_attention(*x[:3], x[4], return_state=True) for x in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got = [F.favor_decay_attention(*x[:3], x[4], return_state=True, stream=s) for x, s in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(refs, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_new_outputs_are_zero_past_the_length():
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(2, 2, 100, 64)
+    n = torch.tensor([40, 0], dtype=torch.int32, device="cuda")
+    out = F.favor_decay_attention(q, k, v, g, lengths=n)
+    assert not out[0, :, 40:].any() and not out[1].any()
+    for x in F.favor_decay_attention_backward(q, k, v, g, do, lengths=n):
+        assert not x[0, :, 40:].any() and not x[1].any()
+
+
+def test_refusals():
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(1, 2, 20, 64)
+    with pytest.raises(TypeError):
+        F.favor_decay_attention(q.half(), k.half(), v.half(), g)
+    with pytest.raises(TypeError):
+        F.favor_decay_attention(q, k.float(), v, g)
+    with pytest.raises(TypeError):
+        F.favor_decay_attention(q, k, v, g.double())
+    with pytest.raises(TypeError):
+        F.favor_decay_attention(q, k, v, None)
+    with pytest.raises(ValueError):
+        F.favor_decay_attention(q, k[:, :1], v, g)
+    with pytest.raises(ValueError):
+        F.favor_decay_attention(q, k, v.transpose(2, 3).contiguous().transpose(2, 3), g)
+    with pytest.raises(TypeError):
+        F.favor_decay_attention(q, k, v, g, lengths=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        F.favor_decay_attention(q, k, v, g, state=torch.zeros(1, 2, 64, 32, device="cuda"))
+    with pytest.raises(F.FavorError):
+        F.favor_decay_attention(q, k, v, g, out=v)
+    with pytest.raises(F.FavorError):
+        F.favor_decay_attention(q, k, v, g, out=q[:, :1].expand_as(q).contiguous()[:, :1].expand_as(q))
+    with pytest.raises(ValueError):
+        F.favor_decay_attention_backward(q, k, v, g, do[:, :, :5])
+    wide = torch.zeros(1, 1, 4, 136, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(F.FavorError) as e:
+        F.favor_decay_attention(wide, wide, wide, g[:1])
+    assert e.value.code == -5
+    torch.cuda.synchronize()
+    assert F.favor_sync_status() == 0
