@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "kernel_decay_step.cuh"
+#include "kernel_decay_tc.cuh"
 #include "kernel_rotary.cuh"
 #include "kernels_decay.cuh"
 
@@ -66,21 +67,54 @@ size_t decay_cc_workspace(int B, int H, int L, int d, int nstates) {
   return (size_t)nstates * B * H * decay_chunks(L) * d * d * sizeof(float);
 }
 
+// A launch that may start while the kernel before it in the stream drains (the kernel waits for that
+// one's results itself) where `pdl` is set.
+template <typename P>
+int launch_with(void (*kern)(P), long long grid, int threads, int smem, cudaStream_t st, bool pdl, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA;
+}
+
+// The scan over `nseg` segments of `seg` tokens whose updates lie in ws.
+int launch_scan(const dcy::Params& p, float* ws, int nseg, int seg, cudaStream_t st) {
+  dcy::ScanParams sp{};
+  for (int i = 0; i < p.nstates; ++i) {
+    sp.in[i] = p.s[i].in;
+    sp.out[i] = p.s[i].out;
+    sp.reverse[i] = p.s[i].reverse;
+  }
+  sp.ws = ws;
+  sp.log_decay = p.log_decay;
+  sp.lengths = p.lengths;
+  sp.nstates = p.nstates, sp.B = p.B, sp.H = p.H, sp.L = p.L, sp.d = p.d, sp.nseg = nseg, sp.seg = seg;
+  const long long grid = ((long long)p.B * p.H * p.nstates * p.d * p.d + dcy::kThreads - 1) / dcy::kThreads;
+  if (grid > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
+  return launch_with(dcy::k_chunk_scan, grid, dcy::kThreads, 0, st, true, sp);
+}
+
 template <typename T, int DP>
 int launch_decay_cc_t(const dcy::Params& p, cudaStream_t st) {
   const long long heads = (long long)p.B * p.H;
   const long long g_up = heads * p.nstates * p.nch, g_out = heads * p.nouts * p.nch;
-  const long long g_scan = (heads * p.nstates * p.d * p.d + dcy::kThreads - 1) / dcy::kThreads;
-  if (g_up > INT_MAX || g_out > INT_MAX || g_scan > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
+  if (g_up > INT_MAX || g_out > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
   auto ku = dcy::k_chunk_update<T, DP>;
   auto ko = dcy::k_chunk_out<T, DP>;
   if (ensure_smem_attr(reinterpret_cast<const void*>(ku), dcy::update_smem(DP)) != FAVOR_OK ||
       ensure_smem_attr(reinterpret_cast<const void*>(ko), dcy::out_smem(DP)) != FAVOR_OK)
     return FAVOR_ERR_CUDA;
-  ku<<<(unsigned)g_up, dcy::kThreads, dcy::update_smem(DP), st>>>(p);
-  dcy::k_chunk_scan<<<(unsigned)g_scan, dcy::kThreads, 0, st>>>(p);
-  ko<<<(unsigned)g_out, dcy::kThreads, dcy::out_smem(DP), st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA;
+  int rc = launch_with<dcy::Params>(ku, g_up, dcy::kThreads, dcy::update_smem(DP), st, false, p);
+  if (rc == FAVOR_OK) rc = launch_scan(p, p.ws, p.nch, dcy::kChunk, st);
+  if (rc == FAVOR_OK) rc = launch_with<dcy::Params>(ko, g_out, dcy::kThreads, dcy::out_smem(DP), st, true, p);
+  return rc;
 }
 
 // The CUDA-core route: every type, head size and stride.
@@ -102,7 +136,144 @@ int launch_decay_cc(dcy::Params p, int dtype_code, cudaStream_t st) {
   return rc;
 }
 
-int launch_decay(const dcy::Params& p, int dtype_code, cudaStream_t st) { return launch_decay_cc(p, dtype_code, st); }
+// ------------------------------------------------------------------ tensor-core route
+// How a call's walk is cut: chunks per segment, segments. `scan`: segment states, the scan and the
+// walk (three launches); else one walk per head from the carried-in state.
+struct WalkPlan {
+  int cps, nseg;
+  bool scan;
+};
+
+// The number of segments with the least estimated time, in chunks of walking: a CTA's start and
+// end cost about two chunks, a chunk of the states alone about 0.6 of a chunk of the walk, the two
+// further launches about three.
+WalkPlan plan_walk(int BH, int L, int nstates, int njobs, bool force_scan) {
+  const int nch = (int)(((long long)L + dtc::kTok - 1) / dtc::kTok), sms = sm_count();
+  auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+  WalkPlan best{};
+  double cost = 1e300;
+  for (int k = 1; k <= std::min(nch, 1024); ++k) {
+    const int cps = (nch + k - 1) / k, nseg = (nch + cps - 1) / cps;
+    if (nseg != k) continue;  // as many segments as the chunks per segment need
+    const bool scan = k > 1 || force_scan;
+    double t = waves((long long)BH * njobs * nseg) * (cps + 2.0);
+    if (scan) t += waves((long long)BH * nstates * nseg) * (0.6 * cps + 2.0) + 3.0 + 0.05 * nseg;
+    if (t < cost) cost = t, best = WalkPlan{cps, nseg, scan};
+    if ((long long)BH * nseg > 8ll * sms) break;
+  }
+  return best;
+}
+
+// Operands the tensor-core route reads in place: bf16 rows and strides of whole 16-byte pieces.
+bool tc_view_ok(const View& v) {
+  const long long lim = 1ll << 39;
+  for (long long s : {v.sb, v.sh, v.st})
+    if (s % 8 != 0 || s >= lim) return false;
+  return true;
+}
+
+bool tc_route(const dcy::Params& p, int dtype_code) {
+  if (dtype_code != 1 || p.d % 8 != 0) return false;
+  for (int i = 0; i < p.nouts; ++i)
+    for (const View* v : {&p.o[i].a, &p.o[i].b, &p.o[i].c, &p.o[i].y})
+      if (!tc_view_ok(*v) || (v != &p.o[i].y && p.L > 1 && v->st == 0)) return false;
+  return true;
+}
+
+// [B][H][L][d] bf16 in boxes of 64 columns x 128 tokens. A dimension an operand repeats over (stride
+// 0) is a dimension of one, walked at coordinate 0: bm, hm.
+bool make_map_view(CUtensorMap* m, int* bm, int* hm, const View& v, int B, int H, int L, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  *bm = v.sb != 0, *hm = v.sh != 0;
+  const cuuint64_t row = (cuuint64_t)(d + 7) / 8 * 16;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)(*hm ? H : 1), (cuuint64_t)(*bm ? B : 1)};
+  const cuuint64_t strides[3] = {v.st ? (cuuint64_t)v.st * 2 : row, v.sh ? (cuuint64_t)v.sh * 2 : row,
+                                 v.sb ? (cuuint64_t)v.sb * 2 : row};
+  const cuuint32_t box[4] = {64, 128, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t walk_workspace(const WalkPlan& pl, int BH, int d, int nstates) {
+  return pl.scan ? (size_t)nstates * BH * pl.nseg * d * d * sizeof(float) : 0;
+}
+
+template <int DP>
+int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaStream_t st) {
+  dtc::Params tp{};
+  int nm = 0;
+  const void* seen[4];
+  long long sst[4][3];
+  // operands by pointer and strides: forward q, k, v; backward q, k, v, dout
+  auto operand = [&](const View& v) -> int {
+    for (int i = 0; i < nm; ++i)
+      if (seen[i] == v.p && sst[i][0] == v.sb && sst[i][1] == v.sh && sst[i][2] == v.st) return i;
+    if (nm == 4 || !make_map_view(&tp.m[nm], &tp.bm[nm], &tp.hm[nm], v, p.B, p.H, p.L, p.d)) return -1;
+    seen[nm] = v.p;
+    sst[nm][0] = v.sb, sst[nm][1] = v.sh, sst[nm][2] = v.st;
+    return nm++;
+  };
+  tp.log_decay = p.log_decay;
+  tp.lengths = p.lengths;
+  tp.B = p.B, tp.H = p.H, tp.L = p.L, tp.d = p.d, tp.nseg = pl.nseg, tp.cps = pl.cps;
+  const long long tasks = (long long)p.B * p.H * pl.nseg;
+  if (tasks * 3 > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
+  if (pl.scan) {
+    using C = dtc::Cfg<DP, false>;
+    auto ks = dtc::k_decay_walk<DP, false>;
+    if (ensure_smem_attr(reinterpret_cast<const void*>(ks), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
+    tp.ws = ws;
+    tp.njobs = p.nstates;
+    for (int i = 0; i < p.nstates; ++i) {
+      tp.j[i].b = operand(p.s[i].b);
+      tp.j[i].c = operand(p.s[i].c);
+      if (tp.j[i].b < 0 || tp.j[i].c < 0) return FAVOR_ERR_CUDA;
+      tp.j[i].state = i;
+      tp.j[i].reverse = p.s[i].reverse;
+    }
+    int rc = launch_with<dtc::Params>(ks, tasks * p.nstates, C::kThreads, C::kSmem, st, false, tp);
+    if (rc == FAVOR_OK) rc = launch_scan(p, ws, pl.nseg, pl.cps * dtc::kTok, st);
+    if (rc != FAVOR_OK) return rc;
+  }
+  using C = dtc::Cfg<DP, true>;
+  auto kw = dtc::k_decay_walk<DP, true>;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(kw), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
+  tp.njobs = p.nouts;
+  for (int i = 0; i < p.nouts; ++i) {
+    dtc::Job& j = tp.j[i];
+    j.a = operand(p.o[i].a);
+    j.b = operand(p.o[i].b);
+    j.c = operand(p.o[i].c);
+    if (j.a < 0 || j.b < 0 || j.c < 0) return FAVOR_ERR_CUDA;
+    j.state = p.o[i].state;
+    j.trans = p.o[i].trans;
+    j.reverse = p.o[i].reverse;
+    j.y = p.o[i].y;
+    j.final = !pl.scan && (i == 0 || p.o[i].state != p.o[i - 1].state);
+  }
+  for (int i = 0; i < p.nstates; ++i) tp.in[i] = p.s[i].in, tp.out[i] = p.s[i].out;
+  return launch_with<dtc::Params>(kw, tasks * p.nouts, C::kThreads, C::kSmem, st, pl.scan, tp);
+}
+
+int launch_decay_tc(const dcy::Params& p, cudaStream_t st) {
+  // two jobs of the backward pass read dstate_out: in place it goes through the scan
+  const bool in_place = p.nouts > 1 && p.s[1].in && p.s[1].in == p.s[1].out;
+  const WalkPlan pl = plan_walk(p.B * p.H, p.L, p.nstates, p.nouts, in_place);
+  void* ws = nullptr;
+  int rc = scratch_alloc(&ws, walk_workspace(pl, p.B * p.H, p.d, p.nstates), st);
+  if (rc != FAVOR_OK) return rc;
+  rc = p.d <= 64 ? launch_decay_tc_t<64>(p, pl, static_cast<float*>(ws), st)
+                 : launch_decay_tc_t<128>(p, pl, static_cast<float*>(ws), st);
+  if (ws) cudaFreeAsync(ws, st);
+  return rc;
+}
+
+int launch_decay(const dcy::Params& p, int dtype_code, cudaStream_t st) {
+  return tc_route(p, dtype_code) ? launch_decay_tc(p, st) : launch_decay_cc(p, dtype_code, st);
+}
 
 bool bad_align(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
@@ -159,7 +330,10 @@ extern "C" {
 
 size_t favor_decay_workspace_bytes(int B, int H, int L, int d, int dtype_code, int backward) {
   if (check_decay_sizes(B, H, L, d, dtype_code) != FAVOR_OK) return 0;
-  return decay_cc_workspace(B, H, L, d, backward ? 2 : 1);
+  const int ns = backward ? 2 : 1;
+  if (dtype_code == 1 && d % 8 == 0)
+    return walk_workspace(plan_walk(B * H, L, ns, backward ? 3 : 1, false), B * H, d, ns);
+  return decay_cc_workspace(B, H, L, d, ns);
 }
 
 int favor_decay_attention(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,

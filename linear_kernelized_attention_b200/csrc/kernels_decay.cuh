@@ -10,13 +10,12 @@
 //   out = (q, k, v, forward), dq = (dout, v, k, forward), dk = (v, dout, q, reverse),
 //   dv = (k, q, dout, reverse).
 //
-// Blocking. Tokens in chunks of kChunk; row r of a chunk with n tokens sees the chunk's carried
-// state X as lambda^r a_r X (forward) or lambda^(n-1-r) a_r X (reverse): X already holds one decay
-// for the step into the chunk, so no exponent is negative and lambda = 0 needs no division.
-//   forward: X_0 = lambda state_in;  X_{c+1} = lambda^n X_c + sum_r lambda^(n-r) b_r c_r^T, and the
-//            last chunk's update takes one decay less, which makes it state_out;
-//   reverse: X_last = dstate_out;    X_{c-1} = lambda^n X_c + sum_r lambda^(r+1) b_r c_r^T, and the
-//            one past chunk 0 is dstate_in.
+// Blocking. Tokens in chunks of kChunk; X is the state a chunk is handed, the sum of its direction's
+// earlier tokens. In a chunk of n tokens, row r sees it as lambda^(r+1) a_r X (forward) or
+// lambda^(n-1-r) a_r X (reverse), and it is handed on as
+//   forward: X' = lambda^n X + sum_r lambda^(n-1-r) b_r c_r^T   (first X: state_in; last X': state_out)
+//   reverse: X' = lambda^n X + sum_r lambda^(r+1) b_r c_r^T     (first X: dstate_out; last X': dstate_in)
+// so no exponent is negative and lambda = 0 needs no division.
 // Three launches: chunk updates (every chunk at once), the scan over chunks (one thread per state
 // element, in double), the outputs (every chunk at once). Powers of lambda are evaluated in double:
 // the library is built with fast single-precision intrinsics.
@@ -27,6 +26,8 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
+
+#include "ptx.cuh"
 
 namespace favor {
 namespace dcy {
@@ -64,6 +65,16 @@ struct Params {
   int nstates, nouts, B, H, L, d, nch;
 };
 
+struct ScanParams {
+  const float* in[2];  // may be null (zeros)
+  float* out[2];       // may be null (not wanted)
+  int reverse[2];
+  float* ws;           // [states][BH][nseg][d * d]
+  const float* log_decay;
+  const int* lengths;
+  int nstates, B, H, L, d, nseg, seg;  // segments, tokens in each
+};
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float& y, float x) { y = x; }
@@ -93,6 +104,7 @@ __device__ __forceinline__ void load_tile(float* dst, const View& x, int b, int 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads) k_chunk_update(const Params p) {
   extern __shared__ float sm[];
+  pdl_launch_dependents();
   float* sb = sm;                 // [kChunk][DP], rows scaled by w_r
   float* sc = sm + kChunk * DP;   // [kChunk][DP]
   const int ch = blockIdx.x % p.nch, q = blockIdx.x / p.nch;
@@ -106,11 +118,10 @@ __global__ void __launch_bounds__(kThreads) k_chunk_update(const Params p) {
   load_tile<T, DP>(sc, job.c, b, h, row0, n, p.d);
   __syncthreads();
   const float g = p.log_decay[h];
-  const int last = !job.reverse && row0 + n == len ? 1 : 0;
   {
     const int r = threadIdx.x >> 2;  // four threads scale one row
     if (r < n) {
-      const float w = (float)decay_pow(g, job.reverse ? r + 1 : n - last - r);
+      const float w = (float)decay_pow(g, job.reverse ? r + 1 : n - 1 - r);
       for (int m = threadIdx.x & 3; m < DP; m += 4) sb[r * DP + m] *= w;
     }
   }
@@ -139,45 +150,35 @@ __global__ void __launch_bounds__(kThreads) k_chunk_update(const Params p) {
       if (m0 + i < p.d && n0 + j < p.d) out[(m0 + i) * p.d + n0 + j] = acc[i][j];
 }
 
-// Each chunk's update replaced by the state carried into it; the boundary states read and written.
-// One thread per (state job, head, element); the running state is held in double.
-static __global__ void __launch_bounds__(kThreads) k_chunk_scan(const Params p) {
+// Each segment's update (p.seg tokens; a chunk is one) replaced by the state it is handed; the
+// boundary states read and written. One thread per (state job, head, element); the running state is
+// held in double.
+static __global__ void __launch_bounds__(kThreads) k_chunk_scan(const __grid_constant__ ScanParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int dd = p.d * p.d;
   const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (e >= (long long)p.nstates * p.B * p.H * dd) return;
   const int el = (int)(e % dd);
   const long long q = e / dd;
   const int bh = (int)(q % (p.B * p.H)), js = (int)(q / (p.B * p.H));
-  const StateJob& job = p.s[js];
   const float g = p.log_decay[bh % p.H];
   const int len = seq_len(p.lengths, bh / p.H, p.L);
-  const int nc = (int)(((long long)len + kChunk - 1) / kChunk);
-  float* u = p.ws + q * p.nch * dd + el;
-  const double x0 = job.in ? (double)job.in[(long long)bh * dd + el] : 0.0;
-  const double full = decay_pow(g, kChunk);
-  double x = x0;
-  if (nc > 0) {
-    const int tail = len - (nc - 1) * kChunk;
-    if (!job.reverse) {
-      if (job.in) x *= decay_pow(g, 1);
-#pragma unroll 4
-      for (int c = 0; c < nc; ++c) {
-        const float w = u[(long long)c * dd];
-        u[(long long)c * dd] = (float)x;
-        x = fma(x, c == nc - 1 ? decay_pow(g, tail - 1) : full, (double)w);
-      }
-    } else {
-      double f = decay_pow(g, tail);
-#pragma unroll 4
-      for (int c = nc - 1; c >= 0; --c) {
-        const float w = u[(long long)c * dd];
-        u[(long long)c * dd] = (float)x;
-        x = fma(x, f, (double)w);
-        f = full;
-      }
+  const int ns = (int)(((long long)len + p.seg - 1) / p.seg);
+  float* u = p.ws + q * p.nseg * dd + el;
+  double x = p.in[js] ? (double)p.in[js][(long long)bh * dd + el] : 0.0;
+  if (ns > 0) {
+    const double full = decay_pow(g, p.seg), tail = decay_pow(g, len - (ns - 1) * p.seg);
+    const int rev = p.reverse[js];
+#pragma unroll 8
+    for (int i = 0; i < ns; ++i) {
+      const int c = rev ? ns - 1 - i : i;
+      const float w = u[(long long)c * dd];
+      u[(long long)c * dd] = (float)x;
+      x = fma(x, c == ns - 1 ? tail : full, (double)w);
     }
   }
-  if (job.out) job.out[(long long)bh * dd + el] = (float)x;
+  if (p.out[js]) p.out[js][(long long)bh * dd + el] = (float)x;
 }
 
 // y rows of one chunk. Grid: outs x BH x chunks, chunk fastest.
@@ -191,13 +192,14 @@ __global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
   float* sb = sa + kChunk * AS;         // [kChunk][AS], then state rows [XR][DP]
   float* sc = sb + kChunk * AS;         // [kChunk][DP]
   float* sp = sc + kChunk * DP;         // [kChunk][PS]
-  float* pw = sp + kChunk * PS;         // lambda^0 .. lambda^63
+  float* pw = sp + kChunk * PS;         // lambda^0 .. lambda^64
   const int ch = blockIdx.x % p.nch, q = blockIdx.x / p.nch;
   const int bh = q % (p.B * p.H), jo = q / (p.B * p.H);
   const int b = bh / p.H, h = bh % p.H;
   const OutJob& job = p.o[jo];
   const int len = seq_len(p.lengths, b, p.L);
   const int row0 = ch * kChunk, n = min(kChunk, len - row0);
+  pdl_wait();
   if (n <= 0) return;
   const int rev = job.reverse;
   auto load_padded = [&](float* dst, const View& x) {
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
   load_padded(sa, job.a);
   load_padded(sb, job.b);
   load_tile<T, DP>(sc, job.c, b, h, row0, n, p.d);
-  if (threadIdx.x < kChunk) pw[threadIdx.x] = (float)decay_pow(p.log_decay[h], threadIdx.x);
+  if (threadIdx.x <= kChunk) pw[threadIdx.x] = (float)decay_pow(p.log_decay[h], threadIdx.x);
   __syncthreads();
 
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i0 + i;
-    const float w = r < n ? pw[rev ? n - 1 - r : r] : 0.f;
+    const float w = r < n ? pw[rev ? n - 1 - r : r + 1] : 0.f;
 #pragma unroll
     for (int j = 0; j < R; ++j) acc[i][j] *= w;
   }
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
 
 constexpr int update_smem(int dp) { return 2 * kChunk * dp * 4; }
 constexpr int out_smem(int dp) {
-  return (2 * kChunk * (dp + 1) + kChunk * dp + kChunk * (kChunk + 1) + kChunk) * 4;
+  return (2 * kChunk * (dp + 1) + kChunk * dp + kChunk * (kChunk + 1) + kChunk + 1) * 4;
 }
 
 }  // namespace dcy
