@@ -56,7 +56,7 @@ struct Job {
 };
 
 struct Params {
-  CUtensorMap m[4];
+  CUtensorMap m[4], my[3];  // operands (boxes of 128 tokens), outputs by job (boxes of 32)
   int bm[4], hm[4];  // 0 where an operand repeats over batch entries or heads
   Job j[3];
   const float* in[2];  // carried-in states, used where `ws` is null
@@ -75,9 +75,12 @@ struct Cfg {
   static constexpr int NS = DP == 64 ? (OUT ? 3 : 4) : 2;
   static constexpr int NLO = DP == 64 ? 2 : 1;
   static constexpr int kLo = NS * kStageB;
-  // d > 64: the image of X and the lo operand share one buffer (the image is read before lo is written)
+  // d > 64: the image of X and the lo operand share one buffer (the image is read before lo is
+  // written), and rows out are staged over the chunk's own A, which every product has read by then.
+  static constexpr int NX = DP == 64 ? 2 : 1;
   static constexpr int kX = DP == 64 ? kLo + NLO * kOpB : kLo;
-  static constexpr int kMisc = kX + (OUT || DP > 64 ? kOpB : 0);
+  static constexpr int kY = kX + (OUT || DP > 64 ? NX * kOpB : 0);
+  static constexpr int kMisc = kY + (OUT && DP == 64 ? kOpB : 0);
   static constexpr int kSmem = kMisc + 2048 + 1024;
   static constexpr int kThreads = OUT ? 640 : 384;
   static constexpr int SB = OUT && DP == 64 ? 2 : 1;  // score buffers
@@ -91,6 +94,7 @@ struct Misc {
   uint32_t tmem_base;
   alignas(16) float pw[132];   // lambda^0 .. lambda^128
   alignas(16) float pwr[32];   // lambda^31 .. lambda^0
+  float pwz[64];               // 31 zeros, then lambda^0 .. lambda^31
   uint64_t full[4], empty[4];
   uint64_t s_full[2], s_free[2], p_full[2];
   uint64_t x_full, qx_done, bh_full[2], u_done[2], o_full, o_free, st_sync, drain;
@@ -104,6 +108,64 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_store_4d(const void* tmap, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
+// MMAs and commits of the one lane with `lead` set, without a branch: the descriptors stay warp-uniform.
+__device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ void unpair(uint64_t v, uint32_t& x, uint32_t& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {  // (low, high) to bf16x2
+  uint32_t x, y;
+  unpair(v, x, y);
+  return pack_bf16x2(__uint_as_float(x), __uint_as_float(y));
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
@@ -144,6 +206,19 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     return;
   }
 
+  auto chunk = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
+  auto tokens = [&](int i) { return min(kTok, len - chunk(i) * kTok); };
+  const int op[3] = {job.b, job.c, job.a};
+  auto load = [&](int i) {  // one lane: chunk i into its stage
+    const int s = i % C::NS, row = chunk(i) * kTok;
+    mbar_arrive_expect_tx(bar(ms->full[s]), C::kStageB);
+#pragma unroll
+    for (int o = 0; o < (OUT ? 3 : 2); ++o)
+#pragma unroll
+      for (int x = 0; x < C::NB; ++x)
+        tma_load_4d(base + s * C::kStageB + o * C::kOpB + x * kAtomB, &p.m[op[o]], bar(ms->full[s]), 64 * x, row,
+                    h * p.hm[op[o]], b * p.bm[op[o]]);
+  };
   if (tid == 0) {
     ms->abort_flag = 0;
     for (int s = 0; s < C::NS; ++s) {
@@ -164,17 +239,20 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     mbar_init(bar(ms->st_sync), 128);
     mbar_init(bar(ms->drain), 1);
     fence_mbar_init();
+    for (int i = 0; i < min(N, C::NS); ++i) load(i);  // in flight while the block sets up
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&ms->tmem_base), C::kCols);
     tmem_relinquish();
   }
-  {
-    const float g = p.log_decay[h];
-    if (tid <= kTok) {
-      const float w = (float)dcy::decay_pow(g, tid);
-      ms->pw[tid] = w;
-      if (tid < 32) ms->pwr[31 - tid] = w;
+  if (tid >= 64 && tid <= 64 + kTok) {
+    const int e = tid - 64;
+    const float w = (float)dcy::decay_pow(p.log_decay[h], e);
+    ms->pw[e] = w;
+    if (e < 32) {
+      ms->pwr[31 - e] = w;
+      ms->pwz[31 + e] = w;
+      if (e < 31) ms->pwz[e] = 0.f;
     }
   }
   tc_fence_before();
@@ -182,29 +260,14 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = ms->tmem_base;
-  auto chunk = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
-  auto tokens = [&](int i) { return min(kTok, len - chunk(i) * kTok); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     const bool leader = elect_one();
-    const int op[3] = {job.b, job.c, job.a};
-    if (leader)
-      for (int o = 0; o < (OUT ? 3 : 2); ++o) tma_prefetch_desc(&p.m[op[o]]);
-    int issued = 0;
-    for (int i = 0; i < N; ++i) {
-      const int s = i % C::NS;
-      if (i >= C::NS && !mbar_wait(bar(ms->empty[s]), ((i / C::NS) - 1) & 1, abort_flag)) break;
-      if (leader) {
-        mbar_arrive_expect_tx(bar(ms->full[s]), C::kStageB);
-        const int row = chunk(i) * kTok;
-#pragma unroll
-        for (int o = 0; o < (OUT ? 3 : 2); ++o)
-#pragma unroll
-          for (int x = 0; x < C::NB; ++x)
-            tma_load_4d(base + s * C::kStageB + o * C::kOpB + x * kAtomB, &p.m[op[o]], bar(ms->full[s]), 64 * x, row,
-                        h * p.hm[op[o]], b * p.bm[op[o]]);
-      }
+    int issued = min(N, C::NS);
+    for (int i = issued; i < N; ++i) {
+      if (!mbar_wait(bar(ms->empty[i % C::NS]), ((i / C::NS) - 1) & 1, abort_flag)) break;
+      if (leader) load(i);
       issued = i + 1;
       __syncwarp();
     }
@@ -214,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    const bool leader = elect_one();
+    const uint32_t lead = elect_one();
     constexpr uint32_t id_s = idesc_f16(128, 128, 1, 1, 0, 0);
     constexpr uint32_t id_x = idesc_f16(128, DP, 1, 1, 0, 1);  // A X and P C
     constexpr uint32_t id_u = idesc_f16(128, DP, 1, 1, 1, 1);
@@ -226,83 +289,81 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
       if (i >= C::SB && !mbar_wait(bar(ms->s_free[sb]), ((i / C::SB) - 1) & 1, abort_flag)) return false;
       tc_fence_after();
-      if (leader) {
-        const uint64_t db = sdesc_sw128(base + s * C::kStageB, 16, 1024);
-        const uint64_t da = sdesc_sw128(base + s * C::kStageB + 2 * C::kOpB, 16, 1024);
+      const uint64_t db = sdesc_sw128(base + s * C::kStageB, 16, 1024);
+      const uint64_t da = sdesc_sw128(base + s * C::kStageB + 2 * C::kOpB, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_ss(tmem + C::kTS + sb * 128, da + kmaj(kk), db + kmaj(kk), id_s, kk > 0 ? 1u : 0u);
-        mma_commit(bar(ms->s_full[sb]));
-      }
-      __syncwarp();
+      for (int kk = 0; kk < DP / 16; ++kk)
+        mma_ss_if(lead, tmem + C::kTS + sb * 128, da + kmaj(kk), db + kmaj(kk), id_s, kk > 0 ? 1u : 0u);
+      commit_if(lead, bar(ms->s_full[sb]));
       return true;
     };
+    // X += (w B)^T C
+    auto update = [&](int i) -> bool {
+      const int s = i % C::NS;
+      if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
+      if (!mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
+      if (!mbar_wait(bar(ms->bh_full[i & 1]), (i >> 1) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t st = base + s * C::kStageB, lo = base + C::kLo + (i % C::NLO) * C::kOpB;
+      const uint64_t dc = sdesc_sw128(st + C::kOpB, kAtomB, 1024);
+      const uint64_t dw = sdesc_sw128(st, DP == 64 ? lo - st : kAtomB, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) mma_ss_if(lead, tmem, dw + kk * kRows16, dc + kk * kRows16, id_u, 1u);
+      if (DP > 64) {
+        const uint64_t dl = sdesc_sw128(lo, kAtomB, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ss_if(lead, tmem, dl + kk * kRows16, dc + kk * kRows16, id_u, 1u);
+      }
+      commit_if(lead, bar(ms->u_done[i & 1]));
+      if (!OUT) commit_if(lead, bar(ms->empty[s]));
+      return true;
+    };
+    // A X
+    auto carried = [&](int i) -> bool {
+      // behind the update (d <= 64) X is there, and x_full may already count the next chunk's
+      if (DP > 64 && !mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
+      if (i >= 1 && !mbar_wait(bar(ms->o_free), (i - 1) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t da = sdesc_sw128(base + (i % C::NS) * C::kStageB + 2 * C::kOpB, 16, 1024);
+      const uint64_t dx = sdesc_sw128(base + C::kX + (i % C::NX) * C::kOpB, kAtomB, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // 128 rows of X: hi and lo (d <= 64), or d
+        mma_ss_if(lead, tmem + C::kTO1, da + kmaj(DP == 64 ? kk & 3 : kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
+      if (DP > 64) commit_if(lead, bar(ms->qx_done));
+      return true;
+    };
+    // P C
+    auto values = [&](int i) -> bool {
+      const int s = i % C::NS, sb = i % C::SB;
+      if (!mbar_wait(bar(ms->p_full[sb]), (i / C::SB) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t dc = sdesc_sw128(base + s * C::kStageB + C::kOpB, kAtomB, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts_if(lead, tmem + C::kTO2, tmem + C::kTS + sb * 128 + 8 * kk, dc + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
+      commit_if(lead, bar(ms->o_full));
+      commit_if(lead, bar(ms->empty[s]));
+      return true;
+    };
+    // The update leads: the next chunk waits for it alone. With one score buffer (d > 64) the next scores
+    // wait for this chunk's rows, and the update for A X, whose image its lo operand overwrites.
     bool ok = !OUT || N <= 0 || scores(0);
     for (int i = 0; ok && i < N; ++i) {
-      const int s = i % C::NS, sb = i % C::SB;
-      const uint32_t st = base + s * C::kStageB;
-      const uint64_t dc = sdesc_sw128(st + C::kOpB, kAtomB, 1024);
-      if (OUT) {
-        if (C::SB == 2 && i + 1 < N && !(ok = scores(i + 1))) break;
-        // A X
-        if (!(ok = mbar_wait(bar(ms->x_full), i & 1, abort_flag))) break;
-        if (i >= 1 && !(ok = mbar_wait(bar(ms->o_free), (i - 1) & 1, abort_flag))) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t da = sdesc_sw128(st + 2 * C::kOpB, 16, 1024);
-          const uint64_t dx = sdesc_sw128(base + C::kX, kAtomB, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 128 rows of X: hi and lo (d <= 64), or d
-            mma_ss(tmem + C::kTO1, da + kmaj(DP == 64 ? kk & 3 : kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
-          if (DP > 64) mma_commit(bar(ms->qx_done));
-        }
-        __syncwarp();
-      } else {
-        if (!(ok = mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag))) break;
-        if (!(ok = mbar_wait(bar(ms->x_full), i & 1, abort_flag))) break;
-      }
-      // X += (w B)^T C
-      if (!(ok = mbar_wait(bar(ms->bh_full[i & 1]), (i >> 1) & 1, abort_flag))) break;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t lo = base + C::kLo + (i % C::NLO) * C::kOpB;
-        if (DP == 64) {
-          const uint64_t dw = sdesc_sw128(st, lo - st, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ss(tmem, dw + kk * kRows16, dc + kk * kRows16, id_u, 1u);
-        } else {
-          const uint64_t dh = sdesc_sw128(st, kAtomB, 1024), dl = sdesc_sw128(lo, kAtomB, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ss(tmem, dh + kk * kRows16, dc + kk * kRows16, id_u, 1u);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ss(tmem, dl + kk * kRows16, dc + kk * kRows16, id_u, 1u);
-        }
-        mma_commit(bar(ms->u_done[i & 1]));
-        if (!OUT) mma_commit(bar(ms->empty[s]));
-      }
-      __syncwarp();
-      if (OUT) {
-        // P C
-        if (!(ok = mbar_wait(bar(ms->p_full[sb]), (i / C::SB) & 1, abort_flag))) break;
-        tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + C::kTO2, tmem + C::kTS + sb * 128 + 8 * kk, dc + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
-          mma_commit(bar(ms->o_full));
-          mma_commit(bar(ms->empty[s]));
-        }
-        __syncwarp();
-        if (C::SB == 1 && i + 1 < N && !(ok = scores(i + 1))) break;
-      }
+      if (!OUT)
+        ok = update(i);
+      else if (C::SB == 2)
+        ok = update(i) && (i + 1 >= N || scores(i + 1)) && carried(i) && values(i);
+      else
+        ok = carried(i) && update(i) && values(i) && (i + 1 >= N || scores(i + 1));
     }
-    if (leader) mma_commit(bar(ms->drain));
+    commit_if(lead, bar(ms->drain));
     __syncwarp();
     mbar_wait(bar(ms->drain), 0, nullptr, kWaitLimitCycles / 8);
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ w B, in place (hi) and beside it (lo)
     const int t = tid - 128;
+    const uint64_t m1 = pair(-1.f, -1.f);
     for (int i = 0; i < N; ++i) {
       const int s = i % C::NS, n = tokens(i);
       if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) break;
@@ -318,13 +379,14 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         uint4 x = *reinterpret_cast<const uint4*>(hi + 16 * e), y;
         if (r < n) {
           const float w = ms->pw[rev ? r + 1 : n - 1 - r];
+          const uint64_t ww = pair(w, w);
           uint32_t* px = &x.x;
           uint32_t* py = &y.x;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float u0 = bf_lo(px[q]) * w, u1 = bf_hi(px[q]) * w;
-            px[q] = pack_bf16x2(u0, u1);
-            py[q] = pack_bf16x2(u0 - bf_lo(px[q]), u1 - bf_hi(px[q]));
+            const uint64_t u = mul2(pair(px[q] << 16, px[q] & 0xffff0000u), ww);
+            px[q] = pack2(u);
+            py[q] = pack2(fma2(pair(px[q] << 16, px[q] & 0xffff0000u), m1, u));
           }
         } else {
           x = y = make_uint4(0u, 0u, 0u, 0u);
@@ -356,6 +418,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       }
       if (i == N && !x_out) break;
       const float f = i < N ? ms->pw[tokens(i)] : 1.f;
+      const uint64_t ff = pair(f, f);
       float* scr = reinterpret_cast<float*>(gb + C::kLo);  // free once the last update is done
 #pragma unroll 1
       for (int x = 0; x < DP / 32; ++x) {
@@ -365,14 +428,20 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int n = 32 * x + e;
-            v[e] = __float_as_uint(x_in && real && n < d ? (job.trans ? x_in[n * d + row] : x_in[row * d + n]) : 0.f);
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+          if (x_in && real && job.trans) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * x + e < d) v[e] = __float_as_uint(x_in[(32 * x + e) * d + row]);
+          } else if (x_in && real) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (32 * x + e < d) *reinterpret_cast<uint4*>(v + e) = *reinterpret_cast<const uint4*>(x_in + row * d + 32 * x + e);
           }
         }
         if (i < N) {
           if (OUT) {
-            uint8_t* img = gb + C::kX + (x >> 1) * kAtomB + row * 128;
+            uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint4 o;
@@ -384,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
             }
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+          for (int e = 0; e < 32; e += 2) unpair(mul2(pair(v[e], v[e + 1]), ff), v[e], v[e + 1]);
           tmem_st32(tmem + la + 32 * x, v);
         } else {
           if (DP == 64) {  // rows 64.. hold the lo products' sums
@@ -436,22 +505,23 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
           tmem_ld32(ts + 32 * x, v);
           tmem_wait_ld();
           if (x == q4) {
+            const float* wz = ms->pwz + 31 + (rev ? -lane : lane);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int gap = rev ? e - lane : lane - e;
-              const float u = __uint_as_float(v[e]) * ms->pw[max(gap, 0)];
-              v[e] = __float_as_uint(gap >= 0 ? u : 0.f);
+            for (int e = 0; e < 32; e += 2) {
+              const uint64_t u = mul2(pair(v[e], v[e + 1]), rev ? pair(wz[e], wz[e + 1]) : pair(wz[-e], wz[-e - 1]));
+              unpair(u, v[e], v[e + 1]);
+              if (rev ? e < lane : e > lane) v[e] = 0u;
+              if (rev ? e + 1 < lane : e + 1 > lane) v[e + 1] = 0u;
             }
           } else {
             // lambda^(i-j) = lambda^(i-32x-31) lambda^(31-(j-32x)), reversed lambda^(32x-i) lambda^(j-32x)
             const float w1 = ms->pw[rev ? 32 * x - row : row - 32 * x - 31];
+            const uint64_t ww = pair(w1, w1);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 w = *reinterpret_cast<const float4*>(wt + e);
-              v[e] = __float_as_uint(__uint_as_float(v[e]) * (w1 * w.x));
-              v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * (w1 * w.y));
-              v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * (w1 * w.z));
-              v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * (w1 * w.w));
+              unpair(mul2(mul2(pair(v[e], v[e + 1]), pair(w.x, w.y)), ww), v[e], v[e + 1]);
+              unpair(mul2(mul2(pair(v[e + 2], v[e + 3]), pair(w.z, w.w)), ww), v[e + 2], v[e + 3]);
             }
           }
           if (rev && n < kTok) {
@@ -480,6 +550,13 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       tc_fence_after();
       const bool live = row < n;
       const float f = ms->pw[live ? (rev ? n - 1 - row : row + 1) : 0];
+      const uint64_t ff = pair(f, f);
+      const bool whole = 32 * q4 + 32 <= n;  // the warp's 32 rows leave as one box
+      const uint32_t slab = (DP == 64 ? C::kY : s * C::kStageB + 2 * C::kOpB) + q4 * 32 * 128;
+      if (DP == 64) {
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+      }
       __nv_bfloat16* yr = y + ((long long)chunk(i) * kTok + row) * job.y.st;
 #pragma unroll 1
       for (int x = 0; x < DP / 32; ++x) {
@@ -487,10 +564,12 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         tmem_ld32(tmem + la + C::kTO2 + 32 * x, o2);
         tmem_ld32(tmem + la + C::kTO1 + 32 * x, o1);
         tmem_wait_ld();
-        float z = 0.f;
+        uint64_t z2 = 0ull;  // NaN if any is not finite
 #pragma unroll
-        for (int e = 0; e < 32; ++e) z = fmaf(__uint_as_float(o2[e]), 0.f, z);  // NaN if any is not finite
-        if (__any_sync(0xffffffffu, live && !(z == 0.f))) {
+        for (int e = 0; e < 32; e += 2) z2 = fma2(pair(o2[e], o2[e + 1]), 0ull, z2);
+        uint32_t za, zb;
+        unpair(z2, za, zb);
+        if (__any_sync(0xffffffffu, live && !(__uint_as_float(za) + __uint_as_float(zb) == 0.f))) {
           // an infinity or NaN in this chunk's c (or P): sum such elements over the row's own tokens
           mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
           const uint8_t* cc = gb + s * C::kStageB + C::kOpB + (x >> 1) * kAtomB;
@@ -521,29 +600,43 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
               if (!(__uint_as_float(o2[8 * q + e]) * 0.f == 0.f)) o2[8 * q + e] = __float_as_uint(acc[e]);
           }
         }
-        if (live) {
+        uint32_t o[16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (32 * x + 8 * q >= d) continue;
-            uint32_t o[4];
+        for (int e = 0; e < 16; ++e) o[e] = pack2(fma2(ff, pair(o1[2 * e], o1[2 * e + 1]), pair(o2[2 * e], o2[2 * e + 1])));
+        if (whole) {
+          uint8_t* ys = gb + slab + (x >> 1) * kAtomB + lane * 128;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = 8 * q + 2 * k;
-              o[k] = pack_bf16x2(fmaf(f, __uint_as_float(o1[e]), __uint_as_float(o2[e])),
-                                 fmaf(f, __uint_as_float(o1[e + 1]), __uint_as_float(o2[e + 1])));
-            }
-            *reinterpret_cast<uint4*>(yr + 32 * x + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(ys + ((((x & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        } else if (live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (32 * x + 8 * q < d)
+              *reinterpret_cast<uint4*>(yr + 32 * x + 8 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
       tc_fence_before();
+      if (whole) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(ms->o_free));
         mbar_arrive(bar(ms->s_free[sb]));
-        mbar_arrive(bar(ms->empty[s]));
+        if (DP == 64) mbar_arrive(bar(ms->empty[s]));
+        if (whole) {
+#pragma unroll
+          for (int x = 0; x < C::NB; ++x)
+            if (64 * x < d)
+              tma_store_4d(&p.my[jid], base + slab + x * kAtomB, 64 * x, chunk(i) * kTok + 32 * q4, h, b);
+          bulk_commit();
+        }
+        if (DP > 64) {
+          bulk_wait_read0();  // the rows lie in the stage
+          mbar_arrive(bar(ms->empty[s]));
+        }
       }
     }
+    if (lane == 0) bulk_wait0();
   }
 
   tc_fence_before();
