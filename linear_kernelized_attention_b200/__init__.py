@@ -377,17 +377,20 @@ def favor_attention_backward_f32(q, k, v, omega, dout, feature_kind=FAVOR_TRIG, 
 
 
 # ---------------------------------------------------------------- linear attention with a decay
-def _rows(name, t, shape, dtype, device):
+# A single-token call costs a few microseconds on the device, so the checks below stay on the few
+# attributes that decide, and errors are worded only once one fails.
+def _operand(name, t, shape, dtype, device):
     """An operand [B, H, L, d] (or [B, H, d]) read in place: any strides, d contiguous."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape or t.device != device:
         raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
 
 
 def _aux(name, t, shape, dtype, device):
@@ -395,7 +398,7 @@ def _aux(name, t, shape, dtype, device):
     import torch
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
         raise TypeError(f"{name} must be a {dtype} tensor on {device}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -404,11 +407,14 @@ def _aux(name, t, shape, dtype, device):
 
 def _strides(*ts):
     """favor_strides of the operands, or None where all are contiguous."""
-    if all(t is None or t.is_contiguous() for t in ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            break
+    else:
         return None
     a = []
     for t in ts:
-        a += [0, 0, 0] if t is None else [*t.stride()[:-1], 0][:3]
+        a += (0, 0, 0) if t is None else (*t.stride()[:-1], 0)[:3]
     return (_ll * len(a))(*a)
 
 
@@ -416,40 +422,38 @@ def _first(name, t, dims):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    dt = t.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dt}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have shape {'[B, H, L, d]' if dims == 4 else '[B, H, d]'}")
-    return 0 if t.dtype == torch.float32 else 1
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return 1 if dt is torch.bfloat16 else 0
 
 
-class _On:
-    """The device of a call's tensors made current, and the stream it launches on: the given one (a
-    stream or its handle), else that device's current one. Tensors made inside belong to that stream."""
+def _elsewhere(device, stream):
+    """A context that makes `stream` (a stream or its handle; None: the device's current one) and the device of
+    the call's tensors current, or None where they are. Tensors made inside belong to that stream."""
+    import torch
+    if stream is None:
+        if torch._C._cuda_getDevice() == device.index:
+            return None
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream) if stream.device == device else torch.cuda.device(device)
 
-    __slots__ = ("ctx", "handle")
 
-    def __init__(self, device, stream):
-        import torch
-        self.ctx = []
-        if torch.cuda.current_device() != device.index:
-            self.ctx.append(torch.cuda.device(device))
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.ctx.append(torch.cuda.stream(stream))
-            self.handle = stream.cuda_stream
+def _handle(device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return self.handle
 
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+def _new(like, zero):
+    import torch
+    make = torch.zeros_like if zero else torch.empty_like
+    return make(like) if like.is_contiguous() else make(like, memory_format=torch.contiguous_format)
 
 
 def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None, state_out=None,
@@ -462,28 +466,29 @@ def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None
     in a new one. state_out may be `state`."""
     import torch
     code = _first("q", q, 4)
-    B, H, L, d = q.shape
     dev = q.device
-    _rows("k", k, q.shape, q.dtype, dev)
-    _rows("v", v, q.shape, q.dtype, dev)
-    _rows("q", q, q.shape, q.dtype, dev)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return favor_decay_attention(q, k, v, log_decay, state, lengths, out, state_out, return_state)
+    shape, dt = q.shape, q.dtype
+    B, H, L, d = shape
+    pk, pv = _operand("k", k, shape, dt, dev), _operand("v", v, shape, dt, dev)
     if log_decay is None:
         raise TypeError("log_decay must be a float32 tensor")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
     s_in = _aux("state", state, (B, H, d, d), torch.float32, dev)
     n = _aux("lengths", lengths, (B,), torch.int32, dev)
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            if lengths is not None:
-                out.zero_()
-        _rows("out", out, q.shape, q.dtype, dev)
-        if state_out is None and return_state:
-            state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
-        s_out = _aux("state_out", state_out, (B, H, d, d), torch.float32, dev)
-        rc = lib().favor_decay_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), g, s_in, n, out.data_ptr(), s_out,
-                                         B, H, L, d, code, _strides(q, k, v, out), handle)
-    _check(rc, "favor_decay_attention")
+    if out is None:
+        out = _new(q, lengths is not None)
+    po = _operand("out", out, shape, dt, dev)
+    if state_out is None and return_state:
+        state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+    s_out = _aux("state_out", state_out, (B, H, d, d), torch.float32, dev)
+    rc = lib().favor_decay_attention(q.data_ptr(), pk, pv, g, s_in, n, po, s_out, B, H, L, d, code,
+                                     _strides(q, k, v, out), _handle(dev))
+    if rc != 0:
+        raise FavorError(rc, "favor_decay_attention")
     return out if state_out is None else (out, state_out)
 
 
@@ -495,33 +500,32 @@ def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=
     as they were in given outputs, and zero in new ones. log_decay gets no gradient."""
     import torch
     code = _first("q", q, 4)
-    B, H, L, d = q.shape
     dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v), ("dout", dout)):
-        _rows(name, t, q.shape, q.dtype, dev)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return favor_decay_attention_backward(q, k, v, log_decay, dout, state, dstate, lengths, dq, dk, dv,
+                                                  dstate_in)
+    shape, dt = q.shape, q.dtype
+    B, H, L, d = shape
+    pk, pv, pdo = (_operand(name, t, shape, dt, dev) for name, t in (("k", k), ("v", v), ("dout", dout)))
     if log_decay is None:
         raise TypeError("log_decay must be a float32 tensor")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
     s_in = _aux("state", state, (B, H, d, d), torch.float32, dev)
     ds = _aux("dstate", dstate, (B, H, d, d), torch.float32, dev)
     n = _aux("lengths", lengths, (B,), torch.int32, dev)
-    with _On(dev, stream) as handle:
-        outs = []
-        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-            if t is None:
-                t = torch.empty_like(q, memory_format=torch.contiguous_format)
-                if lengths is not None:
-                    t.zero_()
-            _rows(name, t, q.shape, q.dtype, dev)
-            outs.append(t)
-        dq, dk, dv = outs
-        if dstate_in is None and (state is not None or dstate is not None):
-            dstate_in = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
-        ds_in = _aux("dstate_in", dstate_in, (B, H, d, d), torch.float32, dev)
-        rc = lib().favor_decay_attention_backward(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g, s_in, n, dout.data_ptr(), ds, dq.data_ptr(), dk.data_ptr(),
-            dv.data_ptr(), ds_in, B, H, L, d, code, _strides(q, k, v, dout, dq, dk, dv), handle)
-    _check(rc, "favor_decay_attention_backward")
+    zero = lengths is not None
+    dq, dk, dv = (_new(q, zero) if t is None else t for t in (dq, dk, dv))
+    pdq, pdk, pdv = (_operand(name, t, shape, dt, dev) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    if dstate_in is None and (state is not None or dstate is not None):
+        dstate_in = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+    ds_in = _aux("dstate_in", dstate_in, (B, H, d, d), torch.float32, dev)
+    rc = lib().favor_decay_attention_backward(
+        q.data_ptr(), pk, pv, g, s_in, n, pdo, ds, pdq, pdk, pdv, ds_in, B, H, L, d, code,
+        _strides(q, k, v, dout, dq, dk, dv), _handle(dev))
+    if rc != 0:
+        raise FavorError(rc, "favor_decay_attention_backward")
     return (dq, dk, dv) if dstate_in is None else (dq, dk, dv, dstate_in)
 
 
@@ -531,21 +535,24 @@ def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
     state: float32 [B, H, d, d]. Returns out [B, H, d]."""
     import torch
     code = _first("q", q, 3)
-    B, H, d = q.shape
     dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _rows(name, t, q.shape, q.dtype, dev)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return favor_decay_step(q, k, v, log_decay, state, out)
+    shape, dt = q.shape, q.dtype
+    B, H, d = shape
+    pk, pv = _operand("k", k, shape, dt, dev), _operand("v", v, shape, dt, dev)
     if log_decay is None or state is None:
         raise TypeError("log_decay and state must be float32 tensors")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
     s = _aux("state", state, (B, H, d, d), torch.float32, dev)
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _rows("out", out, q.shape, q.dtype, dev)
-        rc = lib().favor_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g, s, out.data_ptr(), B, H, d, code,
-                                    _strides(q, k, v, out), handle)
-    _check(rc, "favor_decay_step")
+    if out is None:
+        out = _new(q, False)
+    po = _operand("out", out, shape, dt, dev)
+    rc = lib().favor_decay_step(q.data_ptr(), pk, pv, g, s, po, B, H, d, code, _strides(q, k, v, out), _handle(dev))
+    if rc != 0:
+        raise FavorError(rc, "favor_decay_step")
     return out
 
 
@@ -576,32 +583,36 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
     (q_out, k_out)."""
     import torch
     code = _first("q", q, 4)
-    B, Hq, L, d = q.shape
     dev = q.device
-    _rows("q", q, q.shape, q.dtype, dev)
-    Hk = 0
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return favor_rotary(q, k, freq, positions, first_position, interleaved, inverse, scale, rot_scale, q_out,
+                                k_out)
+    shape, dt = q.shape, q.dtype
+    B, Hq, L, d = shape
+    Hk, pk, pko = 0, None, None
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise TypeError("k must be a CUDA tensor of shape [B, Hk, L, d]")
         Hk = k.shape[1]
-        _rows("k", k, (B, Hk, L, d), q.dtype, dev)
+        pk = _operand("k", k, (B, Hk, L, d), dt, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if freq is None or freq.dim() != 1:
         raise TypeError("freq must be a float64 tensor of shape [rot/2]")
     f = _aux("freq", freq, freq.shape, torch.float64, dev)
     pos = _aux("positions", positions, (B, L), torch.int32, dev)
-    with _On(dev, stream) as handle:
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _rows("q_out", q_out, q.shape, q.dtype, dev)
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-            _rows("k_out", k_out, k.shape, q.dtype, dev)
-        rc = lib().favor_rotary(q.data_ptr(), None if k is None else k.data_ptr(), f, pos, q_out.data_ptr(),
-                                None if k is None else k_out.data_ptr(), B, Hq, Hk, L, d, 2 * freq.numel(),
-                                int(interleaved), int(inverse), int(first_position), scale, rot_scale, code,
-                                _strides(q, k, q_out, k_out), handle)
-    _check(rc, "favor_rotary")
+    if q_out is None:
+        q_out = _new(q, False)
+    pqo = _operand("q_out", q_out, shape, dt, dev)
+    if k is not None:
+        if k_out is None:
+            k_out = _new(k, False)
+        pko = _operand("k_out", k_out, k.shape, dt, dev)
+    rc = lib().favor_rotary(q.data_ptr(), pk, f, pos, pqo, pko, B, Hq, Hk, L, d, 2 * freq.shape[0], int(interleaved),
+                            int(inverse), int(first_position), scale, rot_scale, code, _strides(q, k, q_out, k_out),
+                            _handle(dev))
+    if rc != 0:
+        raise FavorError(rc, "favor_rotary")
     return q_out, k_out
