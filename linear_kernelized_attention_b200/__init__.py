@@ -379,18 +379,25 @@ def favor_attention_backward_f32(q, k, v, omega, dout, feature_kind=FAVOR_TRIG, 
 # ---------------------------------------------------------------- linear attention with a decay
 # A single-token call costs a few microseconds on the device, so the checks below stay on the few
 # attributes that decide, and errors are worded only once one fails.
-def _operand(name, t, shape, dtype, device):
-    """An operand [B, H, L, d] (or [B, H, d]) read in place: any strides, d contiguous."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or t.device != device:
+def _operands(shape, dtype, device, **ts):
+    """Pointers of operands [B, H, L, d] (or [B, H, d]) read in place (any strides, d contiguous), and whether
+    all are contiguous."""
+    ptrs, whole = [], True
+    for name, t in ts.items():
+        try:
+            if t.dtype is dtype and t.shape == shape and t.device == device:
+                if not t.is_contiguous():
+                    whole = False
+                    if t.stride(-1) != 1 and shape[-1] > 1:
+                        raise ValueError(f"{name} must be contiguous in its last dimension")
+                ptrs.append(t.data_ptr())
+                continue
+        except AttributeError:
+            raise TypeError(f"{name} must be a CUDA tensor") from None
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
-    if t.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.data_ptr()
+    return ptrs, whole
 
 
 def _aux(name, t, shape, dtype, device):
@@ -406,12 +413,7 @@ def _aux(name, t, shape, dtype, device):
 
 
 def _strides(*ts):
-    """favor_strides of the operands, or None where all are contiguous."""
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            break
-    else:
-        return None
+    """favor_strides of the operands."""
     a = []
     for t in ts:
         a += (0, 0, 0) if t is None else (*t.stride()[:-1], 0)[:3]
@@ -427,8 +429,6 @@ def _first(name, t, dims):
         raise TypeError(f"{name} must be float32 or bfloat16, got {dt}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have shape {'[B, H, L, d]' if dims == 4 else '[B, H, d]'}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
     return 1 if dt is torch.bfloat16 else 0
 
 
@@ -442,7 +442,9 @@ def _elsewhere(device, stream):
         return torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
-    return torch.cuda.stream(stream) if stream.device == device else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _handle(device):
@@ -473,7 +475,6 @@ def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None
             return favor_decay_attention(q, k, v, log_decay, state, lengths, out, state_out, return_state)
     shape, dt = q.shape, q.dtype
     B, H, L, d = shape
-    pk, pv = _operand("k", k, shape, dt, dev), _operand("v", v, shape, dt, dev)
     if log_decay is None:
         raise TypeError("log_decay must be a float32 tensor")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
@@ -481,12 +482,12 @@ def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None
     n = _aux("lengths", lengths, (B,), torch.int32, dev)
     if out is None:
         out = _new(q, lengths is not None)
-    po = _operand("out", out, shape, dt, dev)
+    (pq, pk, pv, po), whole = _operands(shape, dt, dev, q=q, k=k, v=v, out=out)
     if state_out is None and return_state:
         state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
     s_out = _aux("state_out", state_out, (B, H, d, d), torch.float32, dev)
-    rc = lib().favor_decay_attention(q.data_ptr(), pk, pv, g, s_in, n, po, s_out, B, H, L, d, code,
-                                     _strides(q, k, v, out), _handle(dev))
+    rc = lib().favor_decay_attention(pq, pk, pv, g, s_in, n, po, s_out, B, H, L, d, code,
+                                     None if whole else _strides(q, k, v, out), _handle(dev))
     if rc != 0:
         raise FavorError(rc, "favor_decay_attention")
     return out if state_out is None else (out, state_out)
@@ -508,7 +509,6 @@ def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=
                                                   dstate_in)
     shape, dt = q.shape, q.dtype
     B, H, L, d = shape
-    pk, pv, pdo = (_operand(name, t, shape, dt, dev) for name, t in (("k", k), ("v", v), ("dout", dout)))
     if log_decay is None:
         raise TypeError("log_decay must be a float32 tensor")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
@@ -517,13 +517,13 @@ def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=
     n = _aux("lengths", lengths, (B,), torch.int32, dev)
     zero = lengths is not None
     dq, dk, dv = (_new(q, zero) if t is None else t for t in (dq, dk, dv))
-    pdq, pdk, pdv = (_operand(name, t, shape, dt, dev) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    (pq, pk, pv, pdo, pdq, pdk, pdv), whole = _operands(shape, dt, dev, q=q, k=k, v=v, dout=dout, dq=dq, dk=dk, dv=dv)
     if dstate_in is None and (state is not None or dstate is not None):
         dstate_in = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
     ds_in = _aux("dstate_in", dstate_in, (B, H, d, d), torch.float32, dev)
     rc = lib().favor_decay_attention_backward(
-        q.data_ptr(), pk, pv, g, s_in, n, pdo, ds, pdq, pdk, pdv, ds_in, B, H, L, d, code,
-        _strides(q, k, v, dout, dq, dk, dv), _handle(dev))
+        pq, pk, pv, g, s_in, n, pdo, ds, pdq, pdk, pdv, ds_in, B, H, L, d, code,
+        None if whole else _strides(q, k, v, dout, dq, dk, dv), _handle(dev))
     if rc != 0:
         raise FavorError(rc, "favor_decay_attention_backward")
     return (dq, dk, dv) if dstate_in is None else (dq, dk, dv, dstate_in)
@@ -542,15 +542,15 @@ def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
             return favor_decay_step(q, k, v, log_decay, state, out)
     shape, dt = q.shape, q.dtype
     B, H, d = shape
-    pk, pv = _operand("k", k, shape, dt, dev), _operand("v", v, shape, dt, dev)
     if log_decay is None or state is None:
         raise TypeError("log_decay and state must be float32 tensors")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
     s = _aux("state", state, (B, H, d, d), torch.float32, dev)
     if out is None:
         out = _new(q, False)
-    po = _operand("out", out, shape, dt, dev)
-    rc = lib().favor_decay_step(q.data_ptr(), pk, pv, g, s, po, B, H, d, code, _strides(q, k, v, out), _handle(dev))
+    (pq, pk, pv, po), whole = _operands(shape, dt, dev, q=q, k=k, v=v, out=out)
+    rc = lib().favor_decay_step(pq, pk, pv, g, s, po, B, H, d, code, None if whole else _strides(q, k, v, out),
+                                _handle(dev))
     if rc != 0:
         raise FavorError(rc, "favor_decay_step")
     return out
@@ -591,12 +591,14 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
                                 k_out)
     shape, dt = q.shape, q.dtype
     B, Hq, L, d = shape
-    Hk, pk, pko = 0, None, None
+    Hk, pk, pko, wk = 0, None, None, True
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise TypeError("k must be a CUDA tensor of shape [B, Hk, L, d]")
         Hk = k.shape[1]
-        pk = _operand("k", k, (B, Hk, L, d), dt, dev)
+        if k_out is None:
+            k_out = _new(k, False)
+        (pk, pko), wk = _operands((B, Hk, L, d), dt, dev, k=k, k_out=k_out)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if freq is None or freq.dim() != 1:
@@ -605,14 +607,10 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
     pos = _aux("positions", positions, (B, L), torch.int32, dev)
     if q_out is None:
         q_out = _new(q, False)
-    pqo = _operand("q_out", q_out, shape, dt, dev)
-    if k is not None:
-        if k_out is None:
-            k_out = _new(k, False)
-        pko = _operand("k_out", k_out, k.shape, dt, dev)
-    rc = lib().favor_rotary(q.data_ptr(), pk, f, pos, pqo, pko, B, Hq, Hk, L, d, 2 * freq.shape[0], int(interleaved),
-                            int(inverse), int(first_position), scale, rot_scale, code, _strides(q, k, q_out, k_out),
-                            _handle(dev))
+    (pq, pqo), wq = _operands(shape, dt, dev, q=q, q_out=q_out)
+    rc = lib().favor_rotary(pq, pk, f, pos, pqo, pko, B, Hq, Hk, L, d, 2 * freq.shape[0], int(interleaved), int(inverse),
+                            int(first_position), scale, rot_scale, code,
+                            None if wq and wk else _strides(q, k, q_out, k_out), _handle(dev))
     if rc != 0:
         raise FavorError(rc, "favor_rotary")
     return q_out, k_out

@@ -96,7 +96,7 @@ int launch_scan(const dcy::Params& p, float* ws, int nseg, int seg, cudaStream_t
   sp.log_decay = p.log_decay;
   sp.lengths = p.lengths;
   sp.nstates = p.nstates, sp.B = p.B, sp.H = p.H, sp.L = p.L, sp.d = p.d, sp.nseg = nseg, sp.seg = seg;
-  const long long grid = ((long long)p.B * p.H * p.nstates * p.d * p.d + dcy::kThreads - 1) / dcy::kThreads;
+  const long long grid = (long long)p.B * p.H * p.nstates * ((p.d * p.d + dcy::kThreads - 1) / dcy::kThreads);
   if (grid > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
   return launch_with(dcy::k_chunk_scan, grid, dcy::kThreads, 0, st, true, sp);
 }

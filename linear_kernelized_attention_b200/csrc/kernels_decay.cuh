@@ -152,30 +152,36 @@ __global__ void __launch_bounds__(kThreads) k_chunk_update(const Params p) {
 
 // Each segment's update (p.seg tokens; a chunk is one) replaced by the state it is handed; the
 // boundary states read and written. One thread per (state job, head, element); the running state is
-// held in double.
+// held in double. Eight segments' loads are in flight at a time: the chain itself is one fma a segment.
 static __global__ void __launch_bounds__(kThreads) k_chunk_scan(const __grid_constant__ ScanParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int dd = p.d * p.d;
-  const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (e >= (long long)p.nstates * p.B * p.H * dd) return;
-  const int el = (int)(e % dd);
-  const long long q = e / dd;
-  const int bh = (int)(q % (p.B * p.H)), js = (int)(q / (p.B * p.H));
-  const float g = p.log_decay[bh % p.H];
+  constexpr int G = 8;
+  __shared__ double pw[2];  // lambda^seg, lambda^(tokens of the last segment)
+  const int dd = p.d * p.d, nb = (dd + kThreads - 1) / kThreads;
+  const int q = blockIdx.x / nb, el = (blockIdx.x % nb) * kThreads + threadIdx.x;
+  const int bh = q % (p.B * p.H), js = q / (p.B * p.H);
   const int len = seq_len(p.lengths, bh / p.H, p.L);
   const int ns = (int)(((long long)len + p.seg - 1) / p.seg);
-  float* u = p.ws + q * p.nseg * dd + el;
+  if (threadIdx.x < 64 && threadIdx.x % 32 == 0 && ns > 0)
+    pw[threadIdx.x / 32] = decay_pow(p.log_decay[bh % p.H], threadIdx.x ? len - (ns - 1) * p.seg : p.seg);
+  pdl_launch_dependents();
+  __syncthreads();
+  pdl_wait();
+  if (el >= dd) return;
+  float* u = p.ws + (long long)q * p.nseg * dd + el;
   double x = p.in[js] ? (double)p.in[js][(long long)bh * dd + el] : 0.0;
-  if (ns > 0) {
-    const double full = decay_pow(g, p.seg), tail = decay_pow(g, len - (ns - 1) * p.seg);
-    const int rev = p.reverse[js];
-#pragma unroll 8
-    for (int i = 0; i < ns; ++i) {
-      const int c = rev ? ns - 1 - i : i;
-      const float w = u[(long long)c * dd];
-      u[(long long)c * dd] = (float)x;
-      x = fma(x, c == ns - 1 ? tail : full, (double)w);
+  const int rev = p.reverse[js];
+  for (int i0 = 0; i0 < ns; i0 += G) {
+    float w[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (i0 + i < ns) w[i] = u[(long long)(rev ? ns - 1 - i0 - i : i0 + i) * dd];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int c = rev ? ns - 1 - i0 - i : i0 + i;
+      if (i0 + i < ns) {
+        u[(long long)c * dd] = (float)x;
+        x = fma(x, pw[c == ns - 1], (double)w[i]);
+      }
     }
   }
   if (p.out[js]) p.out[js][(long long)bh * dd + el] = (float)x;
