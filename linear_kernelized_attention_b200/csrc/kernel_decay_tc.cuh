@@ -18,7 +18,8 @@
 // w B to bf16 would cost the fp32 state 2^-9 of every product, so w B goes in as two bf16 terms, hi =
 // bf16(w b) and lo = bf16(w b - hi): 2^-18 per product. hi overwrites B in place once the scores have
 // read it. d <= 64 stacks hi and lo as the 128 rows of one operand (rows 64.. of the state collect the
-// lo products and are added when it is read out); d <= 128 accumulates hi, then lo.
+// lo products and are added when it is read out; its bf16 image for A X, rounded to 2^-8 itself, takes
+// the hi rows alone: 2^-8 once more of each product); d <= 128 accumulates hi, then lo.
 //
 // The state update is the only dependence between chunks: update -> state read and rescaled -> next
 // update, about 1000 cycles against the 2700 in which an SM's share of HBM delivers a d = 64 chunk, so a
@@ -27,8 +28,8 @@
 // segment's own state from b and c alone, k_chunk_scan carries them, and kernel OUT = true walks all
 // segments at once.
 //
-// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-7 w B; 8-11 state; and with OUT 12-15 scores,
-// 16-19 rows out. Thread = row of its 128 (token or state row).
+// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-7 w B; with OUT 8-11 state, 12-15 scores, 16-19
+// rows out; without it 8-11 w B too. Thread = row of its 128 (token or state row).
 //
 // Non-finite values. The mask removes a product by selecting zero into P, but zero times an infinity
 // or NaN in a later token's c would still reach earlier rows of the chunk. Rows out notice a
@@ -171,6 +172,38 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {  // (low, high) to bf16x
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// d <= 64: rows 64.. of the state hold the lo products' sums; one 32-column block of them added to rows
+// 0 .. 63 through `scr` (8 KB), by the 128 threads of the state's rows. False after a timeout.
+__device__ __forceinline__ bool fold_lo(uint32_t (&v)[32], float* scr, int row, Misc* ms, uint32_t& ph) {
+  if (!__all_sync(0xffffffffu, group_sync(smem_u32(&ms->st_sync), ph, &ms->abort_flag))) return false;
+  if (row >= 64) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) scr[e * 64 + row - 64] = __uint_as_float(v[e]);
+  }
+  if (!__all_sync(0xffffffffu, group_sync(smem_u32(&ms->st_sync), ph, &ms->abort_flag))) return false;
+  if (row < 64) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + scr[e * 64 + row]);
+  }
+  return true;
+}
+
+// Columns 32 x .. of one row of X to a [d, d] state, or its transpose.
+__device__ __forceinline__ void store_state(float* out, const uint32_t (&v)[32], int x, int row, int d, int dp,
+                                            int trans) {
+  if (row >= d || row >= dp) return;
+  if (trans) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (32 * x + e < d) out[(32 * x + e) * d + row] = __uint_as_float(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      if (32 * x + e < d)
+        *reinterpret_cast<uint4*>(out + row * d + 32 * x + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+}
+
 template <int DP, bool OUT>
 __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const __grid_constant__ Params p) {
   using C = Cfg<DP, OUT>;
@@ -206,7 +239,9 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     return;
   }
 
-  auto chunk = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
+  // OUT walks with the job's direction; the states alone are summed against it, so that each chunk's
+  // factor (the decay over the segment's tokens beyond it) grows from 1 by one product a chunk
+  auto chunk = [&](int i) { return (rev != 0) == OUT ? c1 - 1 - i : c0 + i; };
   auto tokens = [&](int i) { return min(kTok, len - chunk(i) * kTok); };
   const int op[3] = {job.b, job.c, job.a};
   auto load = [&](int i) {  // one lane: chunk i into its stage
@@ -230,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       mbar_init(bar(ms->s_free[s]), 4);
       mbar_init(bar(ms->p_full[s]), 4);
       mbar_init(bar(ms->u_done[s]), 1);
-      mbar_init(bar(ms->bh_full[s]), 4);
+      mbar_init(bar(ms->bh_full[s]), OUT ? 4 : 8);
     }
     mbar_init(bar(ms->x_full), 4);
     mbar_init(bar(ms->qx_done), 1);
@@ -245,8 +280,8 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     tmem_alloc(smem_u32(&ms->tmem_base), C::kCols);
     tmem_relinquish();
   }
-  if (tid >= 64 && tid <= 64 + kTok) {
-    const int e = tid - 64;
+  if (tid >= 96 && tid <= 96 + kTok) {
+    const int e = tid - 96;
     const float w = (float)dcy::decay_pow(p.log_decay[h], e);
     ms->pw[e] = w;
     if (e < 32) {
@@ -301,14 +336,15 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     auto update = [&](int i) -> bool {
       const int s = i % C::NS;
       if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
-      if (!mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
+      if (OUT && !mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
       if (!mbar_wait(bar(ms->bh_full[i & 1]), (i >> 1) & 1, abort_flag)) return false;
       tc_fence_after();
       const uint32_t st = base + s * C::kStageB, lo = base + C::kLo + (i % C::NLO) * C::kOpB;
       const uint64_t dc = sdesc_sw128(st + C::kOpB, kAtomB, 1024);
       const uint64_t dw = sdesc_sw128(st, DP == 64 ? lo - st : kAtomB, 1024);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) mma_ss_if(lead, tmem, dw + kk * kRows16, dc + kk * kRows16, id_u, 1u);
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ss_if(lead, tmem, dw + kk * kRows16, dc + kk * kRows16, id_u, OUT || i > 0 || kk > 0 ? 1u : 0u);
       if (DP > 64) {
         const uint64_t dl = sdesc_sw128(lo, kAtomB, 1024);
 #pragma unroll
@@ -327,8 +363,8 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       const uint64_t da = sdesc_sw128(base + (i % C::NS) * C::kStageB + 2 * C::kOpB, 16, 1024);
       const uint64_t dx = sdesc_sw128(base + C::kX + (i % C::NX) * C::kOpB, kAtomB, 1024);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // 128 rows of X: hi and lo (d <= 64), or d
-        mma_ss_if(lead, tmem + C::kTO1, da + kmaj(DP == 64 ? kk & 3 : kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < DP / 16; ++kk)
+        mma_ss_if(lead, tmem + C::kTO1, da + kmaj(kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
       if (DP > 64) commit_if(lead, bar(ms->qx_done));
       return true;
     };
@@ -345,70 +381,118 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       commit_if(lead, bar(ms->empty[s]));
       return true;
     };
-    // The update leads: the next chunk waits for it alone. With one score buffer (d > 64) the next scores
-    // wait for this chunk's rows, and the update for A X, whose image its lo operand overwrites.
+    // May scores(i) go out without a wait?
+    auto ready = [&](int i) -> bool {
+      const bool r = mbar_test(bar(ms->full[i % C::NS]), (i / C::NS) & 1) &&
+                     (i < C::SB || mbar_test(bar(ms->s_free[i % C::SB]), ((i / C::SB) - 1) & 1));
+      return __all_sync(0xffffffffu, r);
+    };
+    // With two score buffers the next chunk's scores go ahead where they can, then the update, which the
+    // next chunk waits for. With one (d > 64) they wait for this chunk's rows, and the update for A X,
+    // whose image its lo operand overwrites.
     bool ok = !OUT || N <= 0 || scores(0);
     for (int i = 0; ok && i < N; ++i) {
-      if (!OUT)
+      if (!OUT) {
         ok = update(i);
-      else if (C::SB == 2)
-        ok = update(i) && (i + 1 >= N || scores(i + 1)) && carried(i) && values(i);
-      else
+      } else if (C::SB == 2) {
+        const bool early = i + 1 < N && ready(i + 1);
+        ok = (!early || scores(i + 1)) && update(i) && (early || i + 1 >= N || scores(i + 1)) && carried(i) && values(i);
+      } else {
         ok = carried(i) && update(i) && values(i) && (i + 1 >= N || scores(i + 1));
+      }
     }
     commit_if(lead, bar(ms->drain));
     __syncwarp();
     mbar_wait(bar(ms->drain), 0, nullptr, kWaitLimitCycles / 8);
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < (OUT ? 8 : 12)) {
     // ------------------------------------------------------------ w B, in place (hi) and beside it (lo)
-    const int t = tid - 128;
+    constexpr int T = OUT ? 128 : 256;            // threads
+    constexpr int NR = kTok / (T / 8);            // rows of a thread, T / 8 apart, in every 64 columns
+    const int t = tid - 128, r0 = t >> 3;
     const uint64_t m1 = pair(-1.f, -1.f);
+    float w[NR], cf = 1.f;
+    int nw = 0;  // tokens the weights are for
+    bool ok = true;
     for (int i = 0; i < N; ++i) {
       const int s = i % C::NS, n = tokens(i);
-      if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) break;
-      // the lo buffer's last reader is update i - NLO
-      if (i >= C::NLO && !mbar_wait(bar(ms->u_done[(i - C::NLO) & 1]), ((i - C::NLO) >> 1) & 1, abort_flag)) break;
-      if (OUT && !mbar_wait(bar(ms->s_full[i % C::SB]), (i / C::SB) & 1, abort_flag)) break;  // B has been read
-      if (OUT && DP > 64 && !mbar_wait(bar(ms->qx_done), i & 1, abort_flag)) break;           // so has X's image
-      uint8_t* hi = gb + s * C::kStageB;
-      uint8_t* lo = gb + C::kLo + (i % C::NLO) * C::kOpB;
-#pragma unroll 4
-      for (int e = t; e < C::kOpB / 16; e += 128) {
-        const int r = (e >> 3) & (kTok - 1);
-        uint4 x = *reinterpret_cast<const uint4*>(hi + 16 * e), y;
-        if (r < n) {
-          const float w = ms->pw[rev ? r + 1 : n - 1 - r];
-          const uint64_t ww = pair(w, w);
-          uint32_t* px = &x.x;
-          uint32_t* py = &y.x;
+      if (n != nw || !OUT) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint64_t u = mul2(pair(px[q] << 16, px[q] & 0xffff0000u), ww);
-            px[q] = pack2(u);
-            py[q] = pack2(fma2(pair(px[q] << 16, px[q] & 0xffff0000u), m1, u));
-          }
-        } else {
-          x = y = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < NR; ++k) {
+          const int r = r0 + k * (T / 8);
+          w[k] = r < n ? ms->pw[rev ? r + 1 : n - 1 - r] * cf : 0.f;
         }
-        *reinterpret_cast<uint4*>(hi + 16 * e) = x;
-        *reinterpret_cast<uint4*>(lo + 16 * e) = y;
+        nw = n;
+        if (!OUT) cf *= ms->pw[n];
+      }
+      if (!(ok = mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag))) break;
+      // the lo buffer's last reader is update i - NLO
+      if (i >= C::NLO && !(ok = mbar_wait(bar(ms->u_done[(i - C::NLO) & 1]), ((i - C::NLO) >> 1) & 1, abort_flag))) break;
+      if (OUT && !(ok = mbar_wait(bar(ms->s_full[i % C::SB]), (i / C::SB) & 1, abort_flag))) break;  // B has been read
+      if (OUT && DP > 64 && !(ok = mbar_wait(bar(ms->qx_done), i & 1, abort_flag))) break;           // so has X's image
+      uint8_t* hi = gb + s * C::kStageB + 16 * t;
+      uint8_t* lo = gb + C::kLo + (i % C::NLO) * C::kOpB + 16 * t;
+#pragma unroll 1
+      for (int x = 0; x < C::NB; ++x) {
+#pragma unroll
+        for (int k0 = 0; k0 < NR; k0 += 4) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(hi + x * kAtomB + (k0 + k) * 16 * T);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ww = pair(w[k0 + k], w[k0 + k]);
+            uint32_t px[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, py[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint64_t u = mul2(pair(px[q] << 16, px[q] & 0xffff0000u), ww);
+              px[q] = pack2(u);
+              py[q] = pack2(fma2(pair(px[q] << 16, px[q] & 0xffff0000u), m1, u));
+            }
+            if (n < kTok && r0 + (k0 + k) * (T / 8) >= n) {  // rows behind the end may hold anything
+#pragma unroll
+              for (int q = 0; q < 4; ++q) px[q] = py[q] = 0u;
+            }
+            *reinterpret_cast<uint4*>(hi + x * kAtomB + (k0 + k) * 16 * T) = make_uint4(px[0], px[1], px[2], px[3]);
+            *reinterpret_cast<uint4*>(lo + x * kAtomB + (k0 + k) * 16 * T) = make_uint4(py[0], py[1], py[2], py[3]);
+          }
+        }
       }
       if (n < kTok) {  // rows of c behind the end take part in products with zero: they must be finite
-        uint8_t* cc = hi + C::kOpB;
-        for (int e = t; e < C::kOpB / 16; e += 128)
+        uint8_t* cc = gb + s * C::kStageB + C::kOpB;
+        for (int e = t; e < C::kOpB / 16; e += T)
           if (((e >> 3) & (kTok - 1)) >= n) *reinterpret_cast<uint4*>(cc + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms->bh_full[i & 1]));
     }
-  } else if (warp >= 8 && warp < 12) {
+    if (!OUT && warp < 8) {
+      // the segment's state (thread = row, b's column)
+      const int row = tid - 128;
+      const uint32_t la = uint32_t((warp & 3) * 32) << 16;
+      uint32_t ph = 0;
+      ok = ok && mbar_wait(bar(ms->u_done[(N - 1) & 1]), ((N - 1) >> 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        float* scr = reinterpret_cast<float*>(gb + C::kLo);  // free: the last update is done
+#pragma unroll 1
+        for (int x = 0; x < DP / 32; ++x) {
+          uint32_t v[32];
+          tmem_ld32(tmem + la + 32 * x, v);
+          tmem_wait_ld();
+          if (DP == 64 && !fold_lo(v, scr, row, ms, ph)) break;
+          store_state(x_out, v, x, row, d, DP, job.trans);
+        }
+      }
+    }
+  } else if (OUT && warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ state (thread = row of X, b's column)
     const int q4 = warp & 3, row = q4 * 32 + lane;
     const uint32_t la = uint32_t(q4 * 32) << 16;
-    const bool real = row < d && (DP > 64 || row < 64);
-    if (OUT && x_in) pdl_wait();  // the carried states are written by the kernel before
+    const bool real = row < d;  // d <= 64: rows 64.. are the lo products', from zero
+    if (x_in) pdl_wait();  // the carried states are written by the kernel before
     bool ok = true;
     uint32_t ph = 0;
     for (int i = 0; ok && i <= N; ++i) {
@@ -440,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
           }
         }
         if (i < N) {
-          if (OUT) {
+          if (DP > 64 || row < 64) {
             uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -456,28 +540,13 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
           for (int e = 0; e < 32; e += 2) unpair(mul2(pair(v[e], v[e + 1]), ff), v[e], v[e + 1]);
           tmem_st32(tmem + la + 32 * x, v);
         } else {
-          if (DP == 64) {  // rows 64.. hold the lo products' sums
-            if (!(ok = __all_sync(0xffffffffu, group_sync(bar(ms->st_sync), ph, abort_flag)))) break;
-            if (row >= 64)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) scr[e * 64 + row - 64] = N > 0 ? __uint_as_float(v[e]) : 0.f;
-            if (!(ok = __all_sync(0xffffffffu, group_sync(bar(ms->st_sync), ph, abort_flag)))) break;
-            if (row < 64)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + scr[e * 64 + row]);
-          }
-          if (real) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int n = 32 * x + e;
-              if (n < d) x_out[job.trans ? n * d + row : row * d + n] = __uint_as_float(v[e]);
-            }
-          }
+          if (DP == 64 && !(ok = fold_lo(v, scr, row, ms, ph))) break;
+          store_state(x_out, v, x, row, d, DP, job.trans);
         }
       }
       if (i < N) {
         tmem_wait_st();
-        if (OUT) fence_proxy_async_smem();
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(ms->x_full));
@@ -488,49 +557,59 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     const int q4 = warp & 3, row = q4 * 32 + lane;
     const uint32_t la = uint32_t(q4 * 32) << 16;
     const float* wt = rev ? ms->pw : ms->pwr;
+    float dg[32];  // lambda^|i-j| on the diagonal block, 0 where it is masked
+#pragma unroll
+    for (int e = 0; e < 32; ++e) dg[e] = ms->pwz[31 + (rev ? e - lane : lane - e)];
     for (int i = 0; i < N; ++i) {
       const int sb = i % C::SB, n = tokens(i);
       if (!mbar_wait(bar(ms->s_full[sb]), (i / C::SB) & 1, abort_flag)) break;
       tc_fence_after();
       const uint32_t ts = tmem + la + C::kTS + sb * 128;
-      // P's 16 columns of block x lie in scores that are read or masked by then
+      // In order of columns: P's 16 columns of block x lie in scores that are read, or masked, by then.
 #pragma unroll 1
       for (int x = 0; x < 4; ++x) {
+        if (x == q4) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            uint32_t v[16], pk[8];
+            tmem_ld16(ts + 32 * x + 16 * y, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int j = 16 * y + e;
+              uint32_t u0, u1;
+              unpair(mul2(pair(v[e], v[e + 1]), pair(dg[j], dg[j + 1])), u0, u1);
+              // a masked score may be anything, of a later token or behind the end: selected away
+              if (rev ? j < lane || 32 * x + j >= n : j > lane) u0 = 0u;
+              if (rev ? j + 1 < lane || 32 * x + j + 1 >= n : j + 1 > lane) u1 = 0u;
+              pk[e / 2] = pack_bf16x2(__uint_as_float(u0), __uint_as_float(u1));
+            }
+            tmem_st8(ts + 16 * x + 8 * y, pk);
+          }
+          continue;
+        }
         uint32_t pk[16];
         if (rev ? x < q4 : x > q4) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = 0u;
         } else {
+          // lambda^(i-j) = lambda^(i-32x-31) lambda^(31-(j-32x)), reversed lambda^(32x-i) lambda^(j-32x)
           uint32_t v[32];
           tmem_ld32(ts + 32 * x, v);
+          const float w1 = ms->pw[rev ? 32 * x - row : row - 32 * x - 31];
+          const uint64_t ww = pair(w1, w1);
           tmem_wait_ld();
-          if (x == q4) {
-            const float* wz = ms->pwz + 31 + (rev ? -lane : lane);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t u = mul2(pair(v[e], v[e + 1]), rev ? pair(wz[e], wz[e + 1]) : pair(wz[-e], wz[-e - 1]));
-              unpair(u, v[e], v[e + 1]);
-              if (rev ? e < lane : e > lane) v[e] = 0u;
-              if (rev ? e + 1 < lane : e + 1 > lane) v[e + 1] = 0u;
-            }
-          } else {
-            // lambda^(i-j) = lambda^(i-32x-31) lambda^(31-(j-32x)), reversed lambda^(32x-i) lambda^(j-32x)
-            const float w1 = ms->pw[rev ? 32 * x - row : row - 32 * x - 31];
-            const uint64_t ww = pair(w1, w1);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(wt + e);
-              unpair(mul2(mul2(pair(v[e], v[e + 1]), pair(w.x, w.y)), ww), v[e], v[e + 1]);
-              unpair(mul2(mul2(pair(v[e + 2], v[e + 3]), pair(w.z, w.w)), ww), v[e + 2], v[e + 3]);
-            }
+          for (int e = 0; e < 32; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(wt + e);
+            pk[e / 2] = pack2(mul2(mul2(pair(v[e], v[e + 1]), pair(w.x, w.y)), ww));
+            pk[e / 2 + 1] = pack2(mul2(mul2(pair(v[e + 2], v[e + 3]), pair(w.z, w.w)), ww));
           }
-          if (rev && n < kTok) {
+          if (rev && n < 32 * x + 32) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * x + e >= n) v[e] = 0u;
+            for (int e = 0; e < 16; ++e)
+              pk[e] = 32 * x + 2 * e + 1 < n ? pk[e] : 32 * x + 2 * e < n ? pk[e] & 0xffffu : 0u;
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
         }
         tmem_st16(ts + 16 * x, pk);
       }

@@ -6,13 +6,14 @@ e mag.
   fp32: a product passes at most d roundings in a score or state product, 2 x 128 in chunk sums, one
     for each 128-token chunk it is carried over (`hops`), and ten in weights and joins:
     (d + 266 + hops) 2^-24 mag.
-  bf16 outputs: one rounding of the result (2^-8 |o|), and on the tensor cores one of the weighted
-    scores or of the carried state's image (2^-8 of the products; the decayed operand of the state update
-    keeps 16 bits, 2^-16): 2^-8 |o| + (2^-8 + 2^-16) mag, plus the fp32 terms.
+  bf16 outputs: one rounding of the result (2^-8 |o|), and on the tensor cores one of the weighted scores
+    inside a chunk, or two on the way through the carried state: its image in bf16, and for d <= 64 the
+    image's products of an operand rounded to bf16 (the state itself keeps that operand to 16 bits, 2^-16):
+    2^-8 |o| + (2 x 2^-8 + 2^-16) mag, plus the fp32 terms.
   The elementwise bound is a worst case. Roundings have independent signs, each with a variance of at
     most 2^-16 / 3 of its product's square, so for random inputs the root mean square of the error over
-    a tensor stays within sqrt(2 / 3) 2^-8 of the root mean square of the outputs: the norm test allows
-    twice that for bf16 and 2^-16 for fp32 values made from bf16 operands or fp32 ones.
+    a tensor stays within sqrt(3 / 3) 2^-8 of the root mean square of the outputs: the norm test allows
+    2 sqrt(2 / 3) 2^-8 for bf16 and 2^-16 for fp32 values made from bf16 operands or fp32 ones.
 """
 import numpy as np
 
@@ -50,7 +51,7 @@ def allowed(ref, mag, d, L, bf16_out, tensor_cores=True):
     hops = -(-L // 128)
     a = (d + 266 + hops) * U32 * mag
     if bf16_out:
-        a = a + UBF * np.abs(ref) + ((UBF + UBF * UBF) * mag if tensor_cores else 0.0)
+        a = a + UBF * np.abs(ref) + ((2 * UBF + UBF * UBF) * mag if tensor_cores else 0.0)
     else:
         a = a + UBF * UBF * mag  # states of bf16 operands; fp32 ones keep the first term alone
     return a + 1e-37
