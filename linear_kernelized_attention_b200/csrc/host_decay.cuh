@@ -180,9 +180,10 @@ bool tc_route(const dcy::Params& p, int dtype_code) {
   return true;
 }
 
-// [B][H][L][d] bf16 in boxes of 64 columns x `tokens`. A dimension an operand repeats over (stride
+// [B][H][L][d] bf16 in boxes of 64 columns x 128 tokens (128-byte swizzle), an output in boxes of
+// 32 x 32 (64-byte swizzle). A dimension an operand repeats over (stride
 // 0) is a dimension of one, walked at coordinate 0: bm, hm.
-bool make_map_view(CUtensorMap* m, int* bm, int* hm, const View& v, int B, int H, int L, int d, int tokens) {
+bool make_map_view(CUtensorMap* m, int* bm, int* hm, const View& v, int B, int H, int L, int d, bool output) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   *bm = v.sb != 0, *hm = v.sh != 0;
@@ -190,10 +191,10 @@ bool make_map_view(CUtensorMap* m, int* bm, int* hm, const View& v, int B, int H
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)(*hm ? H : 1), (cuuint64_t)(*bm ? B : 1)};
   const cuuint64_t strides[3] = {v.st ? (cuuint64_t)v.st * 2 : row, v.sh ? (cuuint64_t)v.sh * 2 : row,
                                  v.sb ? (cuuint64_t)v.sb * 2 : row};
-  const cuuint32_t box[4] = {64, (cuuint32_t)tokens, 1, 1};
+  const cuuint32_t box[4] = {output ? 32u : 64u, output ? 32u : 128u, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            output ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -211,7 +212,7 @@ int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaS
   auto operand = [&](const View& v) -> int {
     for (int i = 0; i < nm; ++i)
       if (seen[i] == v.p && sst[i][0] == v.sb && sst[i][1] == v.sh && sst[i][2] == v.st) return i;
-    if (nm == 4 || !make_map_view(&tp.m[nm], &tp.bm[nm], &tp.hm[nm], v, p.B, p.H, p.L, p.d, dtc::kTok))
+    if (nm == 4 || !make_map_view(&tp.m[nm], &tp.bm[nm], &tp.hm[nm], v, p.B, p.H, p.L, p.d, false))
       return -1;
     seen[nm] = v.p;
     sst[nm][0] = v.sb, sst[nm][1] = v.sh, sst[nm][2] = v.st;
@@ -254,7 +255,7 @@ int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaS
     j.reverse = p.o[i].reverse;
     j.y = p.o[i].y;
     int bm, hm;
-    if (!make_map_view(&tp.my[i], &bm, &hm, j.y, p.B, p.H, p.L, p.d, 32)) return FAVOR_ERR_CUDA;
+    if (!make_map_view(&tp.my[i], &bm, &hm, j.y, p.B, p.H, p.L, p.d, true)) return FAVOR_ERR_CUDA;
     j.final = !pl.scan && (i == 0 || p.o[i].state != p.o[i - 1].state);
   }
   for (int i = 0; i < p.nstates; ++i) tp.in[i] = p.s[i].in, tp.out[i] = p.s[i].out;

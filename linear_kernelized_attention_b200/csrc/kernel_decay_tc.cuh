@@ -28,7 +28,7 @@
 // segment's own state from b and c alone, k_chunk_scan carries them, and kernel OUT = true walks all
 // segments at once.
 //
-// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-7 w B; with OUT 8-11 state, 12-15 scores, 16-19
+// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-7 w B; with OUT 8-11 state, 12-19 scores, 20-27
 // rows out; without it 8-11 w B too. Thread = row of its 128 (token or state row).
 //
 // Non-finite values. The mask removes a product by selecting zero into P, but zero times an infinity
@@ -57,7 +57,7 @@ struct Job {
 };
 
 struct Params {
-  CUtensorMap m[4], my[3];  // operands (boxes of 128 tokens), outputs by job (boxes of 32)
+  CUtensorMap m[4], my[3];  // operands (boxes of 64 columns x 128 tokens), outputs by job (32 x 32)
   int bm[4], hm[4];  // 0 where an operand repeats over batch entries or heads
   Job j[3];
   const float* in[2];  // carried-in states, used where `ws` is null
@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr int kY = kX + (OUT || DP > 64 ? NX * kOpB : 0);
   static constexpr int kMisc = kY + (OUT && DP == 64 ? kOpB : 0);
   static constexpr int kSmem = kMisc + 2048 + 1024;
-  static constexpr int kThreads = OUT ? 640 : 384;
+  static constexpr int kThreads = OUT ? 896 : 384;
   static constexpr int SB = OUT && DP == 64 ? 2 : 1;  // score buffers
   static constexpr uint32_t kTO1 = DP, kTO2 = 2 * DP, kTS = DP == 64 ? 192 : 384;
   static constexpr uint32_t kCols = OUT ? 512 : DP;
@@ -93,8 +93,7 @@ struct Cfg {
 struct Misc {
   int abort_flag;
   uint32_t tmem_base;
-  alignas(16) float pw[132];   // lambda^0 .. lambda^128
-  alignas(16) float pwr[32];   // lambda^31 .. lambda^0
+  float pw[132];               // lambda^0 .. lambda^128
   float pwz[64];               // 31 zeros, then lambda^0 .. lambda^31
   uint64_t full[4], empty[4];
   uint64_t s_full[2], s_free[2], p_full[2];
@@ -168,6 +167,9 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {  // (low, high) to bf16x
   unpair(v, x, y);
   return pack_bf16x2(__uint_as_float(x), __uint_as_float(y));
 }
+
+// Column of P's tokens j, j + 1 (bf16 pairs) in their score buffer: each half over its own scores.
+__host__ __device__ constexpr int p_col(int j) { return (j & 64) + ((j & 63) >> 1); }
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -258,19 +260,19 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     ms->abort_flag = 0;
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(bar(ms->full[s]), 1);
-      mbar_init(bar(ms->empty[s]), OUT ? 5 : 1);  // the last MMA's commit; rows out
+      mbar_init(bar(ms->empty[s]), OUT ? 9 : 1);  // the last MMA's commit; rows out
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(ms->s_full[s]), 1);
-      mbar_init(bar(ms->s_free[s]), 4);
-      mbar_init(bar(ms->p_full[s]), 4);
+      mbar_init(bar(ms->s_free[s]), 8);
+      mbar_init(bar(ms->p_full[s]), 8);
       mbar_init(bar(ms->u_done[s]), 1);
       mbar_init(bar(ms->bh_full[s]), OUT ? 4 : 8);
     }
     mbar_init(bar(ms->x_full), 4);
     mbar_init(bar(ms->qx_done), 1);
     mbar_init(bar(ms->o_full), 1);
-    mbar_init(bar(ms->o_free), 4);
+    mbar_init(bar(ms->o_free), 8);
     mbar_init(bar(ms->st_sync), 128);
     mbar_init(bar(ms->drain), 1);
     fence_mbar_init();
@@ -285,7 +287,6 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     const float w = (float)dcy::decay_pow(p.log_decay[h], e);
     ms->pw[e] = w;
     if (e < 32) {
-      ms->pwr[31 - e] = w;
       ms->pwz[31 + e] = w;
       if (e < 31) ms->pwz[e] = 0.f;
     }
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       return true;
     };
     // X += (w B)^T C
-    auto update = [&](int i) -> bool {
+    auto update = [&](int i, bool last) -> bool {  // last: of the chunk's products, as below
       const int s = i % C::NS;
       if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
       if (OUT && !mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         for (int kk = 0; kk < 8; ++kk) mma_ss_if(lead, tmem, dl + kk * kRows16, dc + kk * kRows16, id_u, 1u);
       }
       commit_if(lead, bar(ms->u_done[i & 1]));
-      if (!OUT) commit_if(lead, bar(ms->empty[s]));
+      if (last) commit_if(lead, bar(ms->empty[s]));
       return true;
     };
     // A X
@@ -369,16 +370,16 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       return true;
     };
     // P C
-    auto values = [&](int i) -> bool {
+    auto values = [&](int i, bool last) -> bool {
       const int s = i % C::NS, sb = i % C::SB;
       if (!mbar_wait(bar(ms->p_full[sb]), (i / C::SB) & 1, abort_flag)) return false;
       tc_fence_after();
       const uint64_t dc = sdesc_sw128(base + s * C::kStageB + C::kOpB, kAtomB, 1024);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        mma_ts_if(lead, tmem + C::kTO2, tmem + C::kTS + sb * 128 + 8 * kk, dc + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
+        mma_ts_if(lead, tmem + C::kTO2, tmem + C::kTS + sb * 128 + p_col(16 * kk), dc + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
       commit_if(lead, bar(ms->o_full));
-      commit_if(lead, bar(ms->empty[s]));
+      if (last) commit_if(lead, bar(ms->empty[s]));
       return true;
     };
     // May scores(i) go out without a wait?
@@ -393,12 +394,15 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     bool ok = !OUT || N <= 0 || scores(0);
     for (int i = 0; ok && i < N; ++i) {
       if (!OUT) {
-        ok = update(i);
+        ok = update(i, true);
       } else if (C::SB == 2) {
         const bool early = i + 1 < N && ready(i + 1);
-        ok = (!early || scores(i + 1)) && update(i) && (early || i + 1 >= N || scores(i + 1)) && carried(i) && values(i);
+        ok = (!early || scores(i + 1)) && update(i, false) && (early || i + 1 >= N || scores(i + 1)) && carried(i) &&
+             values(i, true);
       } else {
-        ok = carried(i) && update(i) && values(i) && (i + 1 >= N || scores(i + 1));
+        // rows out start before the update, but where the update's operand pass zeroes c's tail
+        const bool tail = tokens(i) < kTok;
+        ok = carried(i) && (tail ? update(i, false) && values(i, true) : values(i, false) && update(i, true)) && (i + 1 >= N || scores(i + 1));
       }
     }
     commit_if(lead, bar(ms->drain));
@@ -552,58 +556,70 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         if (lane == 0) mbar_arrive(bar(ms->x_full));
       }
     }
-  } else if (OUT && warp >= 12 && warp < 16) {
-    // ------------------------------------------------------------ scores -> P (thread = row)
-    const int q4 = warp & 3, row = q4 * 32 + lane;
+  } else if (OUT && warp >= 12 && warp < 20) {
+    // ------------------------------------------------------------ scores -> P (thread = row, half the columns)
+    const int q4 = warp & 3, row = q4 * 32 + lane, half = (warp - 12) >> 2;
     const uint32_t la = uint32_t(q4 * 32) << 16;
-    const float* wt = rev ? ms->pw : ms->pwr;
-    float dg[32];  // lambda^|i-j| on the diagonal block, 0 where it is masked
-#pragma unroll
-    for (int e = 0; e < 32; ++e) dg[e] = ms->pwz[31 + (rev ? e - lane : lane - e)];
+    const uint64_t l4 = pair(ms->pw[4], ms->pw[4]);
+    const float* wz = ms->pwz + 31 + (rev ? -lane : lane);
     for (int i = 0; i < N; ++i) {
       const int sb = i % C::SB, n = tokens(i);
       if (!mbar_wait(bar(ms->s_full[sb]), (i / C::SB) & 1, abort_flag)) break;
       tc_fence_after();
       const uint32_t ts = tmem + la + C::kTS + sb * 128;
-      // In order of columns: P's 16 columns of block x lie in scores that are read, or masked, by then.
+      // In order of columns: P's 16 columns of block x lie in scores of this half that are read, or
+      // masked, by then.
 #pragma unroll 1
-      for (int x = 0; x < 4; ++x) {
-        if (x == q4) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t v[16], pk[8];
-            tmem_ld16(ts + 32 * x + 16 * y, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int j = 16 * y + e;
-              uint32_t u0, u1;
-              unpair(mul2(pair(v[e], v[e + 1]), pair(dg[j], dg[j + 1])), u0, u1);
-              // a masked score may be anything, of a later token or behind the end: selected away
-              if (rev ? j < lane || 32 * x + j >= n : j > lane) u0 = 0u;
-              if (rev ? j + 1 < lane || 32 * x + j + 1 >= n : j + 1 > lane) u1 = 0u;
-              pk[e / 2] = pack_bf16x2(__uint_as_float(u0), __uint_as_float(u1));
-            }
-            tmem_st8(ts + 16 * x + 8 * y, pk);
-          }
-          continue;
-        }
+      for (int x = 2 * half; x < 2 * half + 2; ++x) {
+        const uint32_t tp = ts + p_col(32 * x);
         uint32_t pk[16];
         if (rev ? x < q4 : x > q4) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = 0u;
         } else {
-          // lambda^(i-j) = lambda^(i-32x-31) lambda^(31-(j-32x)), reversed lambda^(32x-i) lambda^(j-32x)
           uint32_t v[32];
           tmem_ld32(ts + 32 * x, v);
-          const float w1 = ms->pw[rev ? 32 * x - row : row - 32 * x - 31];
-          const uint64_t ww = pair(w1, w1);
-          tmem_wait_ld();
+          if (x == q4) {  // lambda^|i-j|; a masked score may be anything, of a later token or behind the end
+            tmem_wait_ld();
+            if (rev) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(wt + e);
-            pk[e / 2] = pack2(mul2(mul2(pair(v[e], v[e + 1]), pair(w.x, w.y)), ww));
-            pk[e / 2 + 1] = pack2(mul2(mul2(pair(v[e + 2], v[e + 3]), pair(w.z, w.w)), ww));
+              for (int e = 0; e < 32; e += 2) {
+                uint32_t u0, u1;
+                unpair(mul2(pair(v[e], v[e + 1]), pair(wz[e], wz[e + 1])), u0, u1);
+                pk[e / 2] = pack_bf16x2(__uint_as_float(e < lane ? 0u : u0), __uint_as_float(e + 1 < lane ? 0u : u1));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                uint32_t u0, u1;
+                unpair(mul2(pair(v[e], v[e + 1]), pair(wz[-e], wz[-e - 1])), u0, u1);
+                pk[e / 2] = pack_bf16x2(__uint_as_float(e > lane ? 0u : u0), __uint_as_float(e + 1 > lane ? 0u : u1));
+              }
+            }
+          } else {
+            // Weights run along the row by products with lambda^4, from the nearest token outwards: 8 roundings
+            // of 2^-24 under P's own of 2^-8, and no shared-memory reads beside those of the MMAs.
+            const float* near = ms->pw + (rev ? 32 * x - row : row - 32 * x - 31);
+            uint64_t w0 = rev ? pair(near[0], near[1]) : pair(near[1], near[0]);
+            uint64_t w1 = rev ? pair(near[2], near[3]) : pair(near[3], near[2]);
+            tmem_wait_ld();
+            if (rev) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                pk[e / 2] = pack2(mul2(pair(v[e], v[e + 1]), w0));
+                pk[e / 2 + 1] = pack2(mul2(pair(v[e + 2], v[e + 3]), w1));
+                w0 = mul2(w0, l4);
+                w1 = mul2(w1, l4);
+              }
+            } else {
+#pragma unroll
+              for (int e = 28; e >= 0; e -= 4) {
+                pk[e / 2 + 1] = pack2(mul2(pair(v[e + 2], v[e + 3]), w0));
+                pk[e / 2] = pack2(mul2(pair(v[e], v[e + 1]), w1));
+                w0 = mul2(w0, l4);
+                w1 = mul2(w1, l4);
+              }
+            }
           }
           if (rev && n < 32 * x + 32) {
 #pragma unroll
@@ -611,16 +627,16 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
               pk[e] = 32 * x + 2 * e + 1 < n ? pk[e] : 32 * x + 2 * e < n ? pk[e] & 0xffffu : 0u;
           }
         }
-        tmem_st16(ts + 16 * x, pk);
+        tmem_st16(tp, pk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms->p_full[sb]));
     }
-  } else if (OUT && warp >= 16) {
-    // ------------------------------------------------------------ rows out (thread = row)
-    const int q4 = warp & 3, row = q4 * 32 + lane;
+  } else if (OUT && warp >= 20) {
+    // ------------------------------------------------------------ rows out (thread = row, half the columns)
+    const int q4 = warp & 3, row = q4 * 32 + lane, half = (warp - 20) >> 2;
     const uint32_t la = uint32_t(q4 * 32) << 16;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(job.y.p) + b * job.y.sb + h * job.y.sh;
     for (int i = 0; i < N; ++i) {
@@ -630,41 +646,44 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       const bool live = row < n;
       const float f = ms->pw[live ? (rev ? n - 1 - row : row + 1) : 0];
       const uint64_t ff = pair(f, f);
-      const bool whole = 32 * q4 + 32 <= n;  // the warp's 32 rows leave as one box
-      const uint32_t slab = (DP == 64 ? C::kY : s * C::kStageB + 2 * C::kOpB) + q4 * 32 * 128;
+      const bool whole = 32 * q4 + 32 <= n;  // the warp's 32 rows leave as boxes of 32 columns
+      const uint32_t slab = (DP == 64 ? C::kY : s * C::kStageB + 2 * C::kOpB) + q4 * (DP / 32) * 2048;
       if (DP == 64) {
         if (lane == 0) bulk_wait_read0();
         __syncwarp();
       }
       __nv_bfloat16* yr = y + ((long long)chunk(i) * kTok + row) * job.y.st;
 #pragma unroll 1
-      for (int x = 0; x < DP / 32; ++x) {
-        uint32_t o1[32], o2[32];
-        tmem_ld32(tmem + la + C::kTO2 + 32 * x, o2);
-        tmem_ld32(tmem + la + C::kTO1 + 32 * x, o1);
+      for (int g = half * (DP / 32); g < (half + 1) * (DP / 32); ++g) {  // 16 columns
+        uint32_t o1[16], o2[16];
+        tmem_ld16(tmem + la + C::kTO2 + 16 * g, o2);
+        tmem_ld16(tmem + la + C::kTO1 + 16 * g, o1);
         tmem_wait_ld();
-        uint64_t z2 = 0ull;  // NaN if any is not finite
+        uint64_t z2 = 0ull, z3 = 0ull;  // NaN if any is not finite
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) z2 = fma2(pair(o2[e], o2[e + 1]), 0ull, z2);
+        for (int e = 0; e < 16; e += 4) {
+          z2 = fma2(pair(o2[e], o2[e + 1]), 0ull, z2);
+          z3 = fma2(pair(o2[e + 2], o2[e + 3]), 0ull, z3);
+        }
         uint32_t za, zb;
-        unpair(z2, za, zb);
+        unpair(fma2(z3, 0ull, z2), za, zb);
         if (__any_sync(0xffffffffu, live && !(__uint_as_float(za) + __uint_as_float(zb) == 0.f))) {
           // an infinity or NaN in this chunk's c (or P): sum such elements over the row's own tokens
           mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
-          const uint8_t* cc = gb + s * C::kStageB + C::kOpB + (x >> 1) * kAtomB;
+          const uint8_t* cc = gb + s * C::kStageB + C::kOpB + (g >> 2) * kAtomB;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             float acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll 1
             for (int j = 0; j < n; ++j) {
               uint32_t pp;
-              tmem_ld1(tmem + la + C::kTS + sb * 128 + (j >> 1), pp);
+              tmem_ld1(tmem + la + C::kTS + sb * 128 + p_col(j), pp);
               tmem_wait_ld();
               if (rev ? j >= row : j <= row) {
                 const float pj = j & 1 ? bf_hi(pp) : bf_lo(pp);
-                const uint4 u = *reinterpret_cast<const uint4*>(cc + j * 128 + ((((x & 1) * 4 + q) ^ (j & 7)) << 4));
+                const uint4 u = *reinterpret_cast<const uint4*>(cc + j * 128 + ((((g & 3) * 2 + q) ^ (j & 7)) << 4));
                 const uint32_t* pu = &u.x;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -679,20 +698,20 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
               if (!(__uint_as_float(o2[8 * q + e]) * 0.f == 0.f)) o2[8 * q + e] = __float_as_uint(acc[e]);
           }
         }
-        uint32_t o[16];
+        uint32_t o[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = pack2(fma2(ff, pair(o1[2 * e], o1[2 * e + 1]), pair(o2[2 * e], o2[2 * e + 1])));
-        if (whole) {
-          uint8_t* ys = gb + slab + (x >> 1) * kAtomB + lane * 128;
+        for (int e = 0; e < 8; ++e) o[e] = pack2(fma2(ff, pair(o1[2 * e], o1[2 * e + 1]), pair(o2[2 * e], o2[2 * e + 1])));
+        if (whole) {  // 32 rows of 64 bytes, 64-byte swizzle
+          uint8_t* ys = gb + slab + (g >> 1) * 2048 + lane * 64;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(ys + ((((x & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4*>(ys + ((((g & 1) * 2 + q) ^ ((lane >> 1) & 3)) << 4)) =
                 make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         } else if (live) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (32 * x + 8 * q < d)
-              *reinterpret_cast<uint4*>(yr + 32 * x + 8 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          for (int q = 0; q < 2; ++q)
+            if (16 * g + 8 * q < d)
+              *reinterpret_cast<uint4*>(yr + 16 * g + 8 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
       tc_fence_before();
@@ -704,9 +723,8 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         if (DP == 64) mbar_arrive(bar(ms->empty[s]));
         if (whole) {
 #pragma unroll
-          for (int x = 0; x < C::NB; ++x)
-            if (64 * x < d)
-              tma_store_4d(&p.my[jid], base + slab + x * kAtomB, 64 * x, chunk(i) * kTok + 32 * q4, h, b);
+          for (int x = half * (DP / 64); x < (half + 1) * (DP / 64); ++x)
+            if (32 * x < d) tma_store_4d(&p.my[jid], base + slab + x * 2048, 32 * x, chunk(i) * kTok + 32 * q4, h, b);
           bulk_commit();
         }
         if (DP > 64) {
