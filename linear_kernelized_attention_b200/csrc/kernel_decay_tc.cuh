@@ -97,7 +97,7 @@ struct Misc {
   float pwz[64];               // 31 zeros, then lambda^0 .. lambda^31
   uint64_t full[4], empty[4];
   uint64_t s_full[2], s_free[2], p_full[2];
-  uint64_t x_full, qx_done, bh_full[2], u_done[2], o_full, o_free, st_sync, drain;
+  uint64_t x_full, img_full[2], qx_done, bh_full[2], u_done[2], o_full, o_free, st_sync, drain;
 };
 static_assert(sizeof(Misc) <= 2048, "misc block");
 
@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       mbar_init(bar(ms->s_free[s]), 8);
       mbar_init(bar(ms->p_full[s]), 8);
       mbar_init(bar(ms->u_done[s]), 1);
+      mbar_init(bar(ms->img_full[s]), 4);
       mbar_init(bar(ms->bh_full[s]), OUT ? 4 : 8);
     }
     mbar_init(bar(ms->x_full), 4);
@@ -295,7 +296,8 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = ms->tmem_base;
+  // all 512 columns start at column 0; fewer, where the allocator put them
+  const uint32_t tmem = C::kCols == 512 ? 0u : __shfl_sync(0xffffffffu, ms->tmem_base, 0);
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -313,6 +315,9 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
+    // Straight-line for the whole warp: loop counters and descriptors stay in uniform registers, which a
+    // divergent exit on a failed wait would forbid (an MMA then takes about 70 cycles to issue). After a
+    // timeout every wait returns at once and the remaining products run on whatever shared memory holds.
     const uint32_t lead = elect_one();
     constexpr uint32_t id_s = idesc_f16(128, 128, 1, 1, 0, 0);
     constexpr uint32_t id_x = idesc_f16(128, DP, 1, 1, 0, 1);  // A X and P C
@@ -320,10 +325,10 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     constexpr uint64_t kRows16 = (16 * 128) >> 4;  // 16 rows of an MN-major operand
     auto kmaj = [](int kk) { return uint64_t(((kk >> 2) * kAtomB + (kk & 3) * 32) >> 4); };
     // scores of chunk i into buffer i % SB
-    auto scores = [&](int i) -> bool {
+    auto scores = [&](int i) {
       const int s = i % C::NS, sb = i % C::SB;
-      if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
-      if (i >= C::SB && !mbar_wait(bar(ms->s_free[sb]), ((i / C::SB) - 1) & 1, abort_flag)) return false;
+      mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
+      if (i >= C::SB) mbar_wait(bar(ms->s_free[sb]), ((i / C::SB) - 1) & 1, abort_flag);
       tc_fence_after();
       const uint64_t db = sdesc_sw128(base + s * C::kStageB, 16, 1024);
       const uint64_t da = sdesc_sw128(base + s * C::kStageB + 2 * C::kOpB, 16, 1024);
@@ -331,14 +336,13 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       for (int kk = 0; kk < DP / 16; ++kk)
         mma_ss_if(lead, tmem + C::kTS + sb * 128, da + kmaj(kk), db + kmaj(kk), id_s, kk > 0 ? 1u : 0u);
       commit_if(lead, bar(ms->s_full[sb]));
-      return true;
     };
     // X += (w B)^T C
-    auto update = [&](int i, bool last) -> bool {  // last: of the chunk's products, as below
+    auto update = [&](int i, bool last) {  // last: of the chunk's products, as below
       const int s = i % C::NS;
-      if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
-      if (OUT && !mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
-      if (!mbar_wait(bar(ms->bh_full[i & 1]), (i >> 1) & 1, abort_flag)) return false;
+      mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
+      if (OUT) mbar_wait(bar(ms->x_full), i & 1, abort_flag);
+      mbar_wait(bar(ms->bh_full[i & 1]), (i >> 1) & 1, abort_flag);
       tc_fence_after();
       const uint32_t st = base + s * C::kStageB, lo = base + C::kLo + (i % C::NLO) * C::kOpB;
       const uint64_t dc = sdesc_sw128(st + C::kOpB, kAtomB, 1024);
@@ -353,13 +357,11 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       }
       commit_if(lead, bar(ms->u_done[i & 1]));
       if (last) commit_if(lead, bar(ms->empty[s]));
-      return true;
     };
     // A X
-    auto carried = [&](int i) -> bool {
-      // behind the update (d <= 64) X is there, and x_full may already count the next chunk's
-      if (DP > 64 && !mbar_wait(bar(ms->x_full), i & 1, abort_flag)) return false;
-      if (i >= 1 && !mbar_wait(bar(ms->o_free), (i - 1) & 1, abort_flag)) return false;
+    auto carried = [&](int i) {
+      mbar_wait(bar(ms->img_full[i & 1]), (i >> 1) & 1, abort_flag);
+      if (i >= 1) mbar_wait(bar(ms->o_free), (i - 1) & 1, abort_flag);
       tc_fence_after();
       const uint64_t da = sdesc_sw128(base + (i % C::NS) * C::kStageB + 2 * C::kOpB, 16, 1024);
       const uint64_t dx = sdesc_sw128(base + C::kX + (i % C::NX) * C::kOpB, kAtomB, 1024);
@@ -367,12 +369,11 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       for (int kk = 0; kk < DP / 16; ++kk)
         mma_ss_if(lead, tmem + C::kTO1, da + kmaj(kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
       if (DP > 64) commit_if(lead, bar(ms->qx_done));
-      return true;
     };
     // P C
-    auto values = [&](int i, bool last) -> bool {
+    auto values = [&](int i, bool last) {
       const int s = i % C::NS, sb = i % C::SB;
-      if (!mbar_wait(bar(ms->p_full[sb]), (i / C::SB) & 1, abort_flag)) return false;
+      mbar_wait(bar(ms->p_full[sb]), (i / C::SB) & 1, abort_flag);
       tc_fence_after();
       const uint64_t dc = sdesc_sw128(base + s * C::kStageB + C::kOpB, kAtomB, 1024);
 #pragma unroll
@@ -380,7 +381,6 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         mma_ts_if(lead, tmem + C::kTO2, tmem + C::kTS + sb * 128 + p_col(16 * kk), dc + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
       commit_if(lead, bar(ms->o_full));
       if (last) commit_if(lead, bar(ms->empty[s]));
-      return true;
     };
     // May scores(i) go out without a wait?
     auto ready = [&](int i) -> bool {
@@ -391,18 +391,25 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     // With two score buffers the next chunk's scores go ahead where they can, then the update, which the
     // next chunk waits for. With one (d > 64) they wait for this chunk's rows, and the update for A X,
     // whose image its lo operand overwrites.
-    bool ok = !OUT || N <= 0 || scores(0);
-    for (int i = 0; ok && i < N; ++i) {
+    if (OUT && N > 0) scores(0);
+    for (int i = 0; i < N; ++i) {
       if (!OUT) {
-        ok = update(i, true);
+        update(i, true);
       } else if (C::SB == 2) {
         const bool early = i + 1 < N && ready(i + 1);
-        ok = (!early || scores(i + 1)) && update(i, false) && (early || i + 1 >= N || scores(i + 1)) && carried(i) &&
-             values(i, true);
+        if (early) scores(i + 1);
+        update(i, false);
+        if (!early && i + 1 < N) scores(i + 1);
+        carried(i);
+        values(i, true);
       } else {
         // rows out start before the update, but where the update's operand pass zeroes c's tail
         const bool tail = tokens(i) < kTok;
-        ok = carried(i) && (tail ? update(i, false) && values(i, true) : values(i, false) && update(i, true)) && (i + 1 >= N || scores(i + 1));
+        carried(i);
+        if (tail) update(i, false);
+        values(i, tail);
+        if (!tail) update(i, true);
+        if (i + 1 < N) scores(i + 1);
       }
     }
     commit_if(lead, bar(ms->drain));
@@ -531,14 +538,10 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
           if (DP > 64 || row < 64) {
             uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 o;
-              o.x = pack_bf16x2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1]));
-              o.y = pack_bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3]));
-              o.z = pack_bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5]));
-              o.w = pack_bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]));
-              *reinterpret_cast<uint4*>(img + ((((x & 1) * 4 + q) ^ (row & 7)) << 4)) = o;
-            }
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(img + ((((x & 1) * 4 + q) ^ (row & 7)) << 4)) =
+                  make_uint4(pack2(pair(v[8 * q], v[8 * q + 1])), pack2(pair(v[8 * q + 2], v[8 * q + 3])),
+                             pack2(pair(v[8 * q + 4], v[8 * q + 5])), pack2(pair(v[8 * q + 6], v[8 * q + 7])));
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) unpair(mul2(pair(v[e], v[e + 1]), ff), v[e], v[e + 1]);
@@ -550,10 +553,12 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       }
       if (i < N) {
         tmem_wait_st();
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ms->x_full));
+        if (lane == 0) mbar_arrive(bar(ms->x_full));  // the update may go ahead
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ms->img_full[i & 1]));
       }
     }
   } else if (OUT && warp >= 12 && warp < 20) {
@@ -641,6 +646,10 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(job.y.p) + b * job.y.sb + h * job.y.sh;
     for (int i = 0; i < N; ++i) {
       const int s = i % C::NS, sb = i % C::SB, n = tokens(i);
+      if (DP == 64) {
+        if (lane == 0) bulk_wait_read0();  // the last chunk's rows have left their place
+        __syncwarp();
+      }
       if (!mbar_wait(bar(ms->o_full), i & 1, abort_flag)) break;
       tc_fence_after();
       const bool live = row < n;
@@ -648,10 +657,6 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       const uint64_t ff = pair(f, f);
       const bool whole = 32 * q4 + 32 <= n;  // the warp's 32 rows leave as boxes of 32 columns
       const uint32_t slab = (DP == 64 ? C::kY : s * C::kStageB + 2 * C::kOpB) + q4 * (DP / 32) * 2048;
-      if (DP == 64) {
-        if (lane == 0) bulk_wait_read0();
-        __syncwarp();
-      }
       __nv_bfloat16* yr = y + ((long long)chunk(i) * kTok + row) * job.y.st;
 #pragma unroll 1
       for (int g = half * (DP / 32); g < (half + 1) * (DP / 32); ++g) {  // 16 columns
@@ -715,12 +720,15 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         }
       }
       tc_fence_before();
-      if (whole) fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0) {  // the accumulators, scores and c are read
         mbar_arrive(bar(ms->o_free));
         mbar_arrive(bar(ms->s_free[sb]));
         if (DP == 64) mbar_arrive(bar(ms->empty[s]));
+      }
+      if (whole) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
         if (whole) {
 #pragma unroll
           for (int x = half * (DP / 64); x < (half + 1) * (DP / 64); ++x)
