@@ -253,7 +253,7 @@ int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaS
     j.state = p.o[i].state;
     j.trans = p.o[i].trans;
     j.reverse = p.o[i].reverse;
-    j.y = p.o[i].y;
+    j.va = p.o[i].a, j.vb = p.o[i].b, j.vc = p.o[i].c, j.y = p.o[i].y;
     int bm, hm;
     if (!make_map_view(&tp.my[i], &bm, &hm, j.y, p.B, p.H, p.L, p.d, true)) return FAVOR_ERR_CUDA;
     j.final = !pl.scan && (i == 0 || p.o[i].state != p.o[i - 1].state);

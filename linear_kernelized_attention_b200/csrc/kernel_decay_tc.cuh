@@ -33,7 +33,8 @@
 //
 // Non-finite values. The mask removes a product by selecting zero into P, but zero times an infinity
 // or NaN in a later token's c would still reach earlier rows of the chunk. Rows out notice a
-// non-finite P C and sum that element again over its own tokens alone. Rows of c behind the
+// non-finite P C and sum that element again, from global memory, over its own tokens alone, so that
+// nothing on chip waits for them. Rows of c behind the
 // sequence's end are zeroed in shared memory.
 #pragma once
 #include <cuda_bf16.h>
@@ -53,7 +54,7 @@ struct Job {
   int a, b, c;  // operands (indices into Params::m)
   int state, trans, reverse;
   int final;    // 1: writes its state's `out` (one segment only)
-  View y;
+  View va, vb, vc, y;  // rows in global memory: a, b, c for elements summed again
 };
 
 struct Params {
@@ -96,8 +97,8 @@ struct Misc {
   float pw[132];               // lambda^0 .. lambda^128
   float pwz[64];               // 31 zeros, then lambda^0 .. lambda^31
   uint64_t full[4], empty[4];
-  uint64_t s_full[2], s_free[2], p_full[2];
-  uint64_t x_full, img_full[2], qx_done, bh_full[2], u_done[2], o_full, o_free, st_sync, drain;
+  uint64_t s_full[2], p_full[2];
+  uint64_t x_full, img_full[2], qx_done, pc_done[2], bh_full[2], u_done[2], o_full, o_free, st_sync, drain;
 };
 static_assert(sizeof(Misc) <= 2048, "misc block");
 
@@ -173,6 +174,16 @@ __host__ __device__ constexpr int p_col(int j) { return (j & 64) + ((j & 63) >> 
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// One token's row of an operand, and eight of its elements.
+__device__ __forceinline__ const __nv_bfloat16* row_of(const View& v, int b, int h, long long t) {
+  return static_cast<const __nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + t * v.st;
+}
+__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  x[0] = bf_lo(u.x), x[1] = bf_hi(u.x), x[2] = bf_lo(u.y), x[3] = bf_hi(u.y);
+  x[4] = bf_lo(u.z), x[5] = bf_hi(u.z), x[6] = bf_lo(u.w), x[7] = bf_hi(u.w);
+}
 
 // d <= 64: rows 64.. of the state hold the lo products' sums; one 32-column block of them added to rows
 // 0 .. 63 through `scr` (8 KB), by the 128 threads of the state's rows. False after a timeout.
@@ -260,12 +271,12 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     ms->abort_flag = 0;
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(bar(ms->full[s]), 1);
-      mbar_init(bar(ms->empty[s]), OUT ? 9 : 1);  // the last MMA's commit; rows out
+      mbar_init(bar(ms->empty[s]), OUT && DP > 64 ? 9 : 1);  // the last MMA's commit; rows staged over a
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(ms->s_full[s]), 1);
-      mbar_init(bar(ms->s_free[s]), 8);
       mbar_init(bar(ms->p_full[s]), 8);
+      mbar_init(bar(ms->pc_done[s]), 1);
       mbar_init(bar(ms->u_done[s]), 1);
       mbar_init(bar(ms->img_full[s]), 4);
       mbar_init(bar(ms->bh_full[s]), OUT ? 4 : 8);
@@ -328,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     auto scores = [&](int i) {
       const int s = i % C::NS, sb = i % C::SB;
       mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
-      if (i >= C::SB) mbar_wait(bar(ms->s_free[sb]), ((i / C::SB) - 1) & 1, abort_flag);
+      if (i >= C::SB) mbar_wait(bar(ms->pc_done[sb]), ((i / C::SB) - 1) & 1, abort_flag);
       tc_fence_after();
       const uint64_t db = sdesc_sw128(base + s * C::kStageB, 16, 1024);
       const uint64_t da = sdesc_sw128(base + s * C::kStageB + 2 * C::kOpB, 16, 1024);
@@ -380,30 +391,23 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       for (int kk = 0; kk < 8; ++kk)
         mma_ts_if(lead, tmem + C::kTO2, tmem + C::kTS + sb * 128 + p_col(16 * kk), dc + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
       commit_if(lead, bar(ms->o_full));
+      commit_if(lead, bar(ms->pc_done[sb]));
       if (last) commit_if(lead, bar(ms->empty[s]));
     };
-    // May scores(i) go out without a wait?
-    auto ready = [&](int i) -> bool {
-      const bool r = mbar_test(bar(ms->full[i % C::NS]), (i / C::NS) & 1) &&
-                     (i < C::SB || mbar_test(bar(ms->s_free[i % C::SB]), ((i / C::SB) - 1) & 1));
-      return __all_sync(0xffffffffu, r);
-    };
-    // With two score buffers the next chunk's scores go ahead where they can, then the update, which the
-    // next chunk waits for. With one (d > 64) they wait for this chunk's rows, and the update for A X,
-    // whose image its lo operand overwrites.
+    // The next chunk's scores go first: they wait for the products P C that read their buffer, no more.
+    // With one score buffer (d > 64) that is this chunk's; and the update follows A X, whose image its lo
+    // operand overwrites, and P C, which lets the rows out start, but where the update's operand pass
+    // zeroes c's tail.
     if (OUT && N > 0) scores(0);
     for (int i = 0; i < N; ++i) {
       if (!OUT) {
         update(i, true);
       } else if (C::SB == 2) {
-        const bool early = i + 1 < N && ready(i + 1);
-        if (early) scores(i + 1);
+        if (i + 1 < N) scores(i + 1);
         update(i, false);
-        if (!early && i + 1 < N) scores(i + 1);
         carried(i);
         values(i, true);
       } else {
-        // rows out start before the update, but where the update's operand pass zeroes c's tail
         const bool tail = tokens(i) < kTok;
         carried(i);
         if (tail) update(i, false);
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     const uint32_t la = uint32_t(q4 * 32) << 16;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(job.y.p) + b * job.y.sb + h * job.y.sh;
     for (int i = 0; i < N; ++i) {
-      const int s = i % C::NS, sb = i % C::SB, n = tokens(i);
+      const int s = i % C::NS, n = tokens(i);
       if (DP == 64) {
         if (lane == 0) bulk_wait_read0();  // the last chunk's rows have left their place
         __syncwarp();
@@ -673,35 +677,40 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         uint32_t za, zb;
         unpair(fma2(z3, 0ull, z2), za, zb);
         if (__any_sync(0xffffffffu, live && !(__uint_as_float(za) + __uint_as_float(zb) == 0.f))) {
-          // an infinity or NaN in this chunk's c (or P): sum such elements over the row's own tokens
-          mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
-          const uint8_t* cc = gb + s * C::kStageB + C::kOpB + (g >> 2) * kAtomB;
-#pragma unroll
+          // an infinity or NaN in this chunk's a, b or c: sum such elements over the row's own tokens
+          const long long t0 = (long long)chunk(i) * kTok;
+          const __nv_bfloat16* ga = row_of(job.va, b, h, t0 + (live ? row : 0));
+#pragma unroll 1
           for (int q = 0; q < 2; ++q) {
+            const int col = 16 * g + 8 * q;
+            if (col >= d || !live) continue;
             float acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+            const int j1 = rev ? n : row + 1;
 #pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-              uint32_t pp;
-              tmem_ld1(tmem + la + C::kTS + sb * 128 + p_col(j), pp);
-              tmem_wait_ld();
-              if (rev ? j >= row : j <= row) {
-                const float pj = j & 1 ? bf_hi(pp) : bf_lo(pp);
-                const uint4 u = *reinterpret_cast<const uint4*>(cc + j * 128 + ((((g & 3) * 2 + q) ^ (j & 7)) << 4));
-                const uint32_t* pu = &u.x;
+            for (int j = rev ? row : 0; j < j1; ++j) {
+              const __nv_bfloat16* gbj = row_of(job.vb, b, h, t0 + j);
+              float sc = 0.f;
+#pragma unroll 1
+              for (int m = 0; m < d; m += 8) {
+                float x[8], z[8];
+                load8(x, ga + m);
+                load8(z, gbj + m);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  acc[2 * k] = fmaf(pj, bf_lo(pu[k]), acc[2 * k]);
-                  acc[2 * k + 1] = fmaf(pj, bf_hi(pu[k]), acc[2 * k + 1]);
-                }
+                for (int e = 0; e < 8; ++e) sc = fmaf(x[e], z[e], sc);
               }
-              __syncwarp();
+              sc *= ms->pw[rev ? j - row : row - j];
+              float z[8];
+              load8(z, row_of(job.vc, b, h, t0 + j) + col);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[e] = fmaf(sc, z[e], acc[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (!(__uint_as_float(o2[8 * q + e]) * 0.f == 0.f)) o2[8 * q + e] = __float_as_uint(acc[e]);
+            for (int e = 0; e < 16; ++e)
+              if ((e >> 3) == q && !(__uint_as_float(o2[e]) * 0.f == 0.f)) o2[e] = __float_as_uint(acc[e & 7]);
           }
+          __syncwarp();
         }
         uint32_t o[8];
 #pragma unroll
@@ -721,11 +730,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {  // the accumulators, scores and c are read
-        mbar_arrive(bar(ms->o_free));
-        mbar_arrive(bar(ms->s_free[sb]));
-        if (DP == 64) mbar_arrive(bar(ms->empty[s]));
-      }
+      if (lane == 0) mbar_arrive(bar(ms->o_free));  // the accumulators are read
       if (whole) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
