@@ -28,8 +28,8 @@
 // segment's own state from b and c alone, k_chunk_scan carries them, and kernel OUT = true walks all
 // segments at once.
 //
-// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-7 w B; with OUT 8-11 state, 12-19 scores, 20-27
-// rows out; without it 8-11 w B too. Thread = row of its 128 (token or state row).
+// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-11 w B and state; with OUT 12-19 scores, 20-27
+// rows out. Thread = row of its 128 (token or state row).
 //
 // Non-finite values. The mask removes a product by selecting zero into P, but zero times an infinity
 // or NaN in a later token's c would still reach earlier rows of the chunk. Rows out notice a
@@ -85,6 +85,7 @@ struct Cfg {
   static constexpr int kMisc = kY + (OUT && DP == 64 ? kOpB : 0);
   static constexpr int kSmem = kMisc + 2048 + 1024;
   static constexpr int kThreads = OUT ? 896 : 384;
+  static constexpr int kBT = OUT && DP == 64 ? 128 : 256;  // threads that weight B
   static constexpr int SB = OUT && DP == 64 ? 2 : 1;  // score buffers
   static constexpr uint32_t kTO1 = DP, kTO2 = 2 * DP, kTS = DP == 64 ? 192 : 384;
   static constexpr uint32_t kCols = OUT ? 512 : DP;
@@ -201,6 +202,25 @@ __device__ __forceinline__ bool fold_lo(uint32_t (&v)[32], float* scr, int row, 
   return true;
 }
 
+// Columns 32 x .. of one row of X from a [d, d] state, or its transpose; zeros where there is none.
+__device__ __forceinline__ void load_state(uint32_t (&v)[32], const float* in, int x, int row, int d, int trans) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = 0u;
+  if (!in || row >= d) return;  // d <= 64: rows 64.. are the lo products', from zero
+  if (trans) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (32 * x + e < d) v[e] = __float_as_uint(in[(32 * x + e) * d + row]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      if (32 * x + e < d) {
+        const uint4 u = *reinterpret_cast<const uint4*>(in + row * d + 32 * x + e);
+        v[e] = u.x, v[e + 1] = u.y, v[e + 2] = u.z, v[e + 3] = u.w;
+      }
+  }
+}
+
 // Columns 32 x .. of one row of X to a [d, d] state, or its transpose.
 __device__ __forceinline__ void store_state(float* out, const uint32_t (&v)[32], int x, int row, int d, int dp,
                                             int trans) {
@@ -278,10 +298,10 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       mbar_init(bar(ms->p_full[s]), 8);
       mbar_init(bar(ms->pc_done[s]), 1);
       mbar_init(bar(ms->u_done[s]), 1);
-      mbar_init(bar(ms->img_full[s]), 4);
-      mbar_init(bar(ms->bh_full[s]), OUT ? 4 : 8);
+      mbar_init(bar(ms->img_full[s]), DP / 16);
+      mbar_init(bar(ms->bh_full[s]), C::kBT / 32);
     }
-    mbar_init(bar(ms->x_full), 4);
+    mbar_init(bar(ms->x_full), DP / 16);
     mbar_init(bar(ms->qx_done), 1);
     mbar_init(bar(ms->o_full), 1);
     mbar_init(bar(ms->o_free), 8);
@@ -420,16 +440,24 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     __syncwarp();
     mbar_wait(bar(ms->drain), 0, nullptr, kWaitLimitCycles / 8);
     __syncwarp();
-  } else if (warp >= 4 && warp < (OUT ? 8 : 12)) {
-    // ------------------------------------------------------------ w B, in place (hi) and beside it (lo)
-    constexpr int T = OUT ? 128 : 256;            // threads
-    constexpr int NR = kTok / (T / 8);            // rows of a thread, T / 8 apart, in every 64 columns
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ w B and the state
+    // w B in place (hi) and beside it (lo); thread = every (T / 8)-th row of each 64 columns.
+    // State: thread = row of X (b's column). d <= 64: one warpgroup each, side by side. d > 64: the update
+    // waits for w B, w B for A X (its lo lies over X's image) and A X for the state, so both warpgroups
+    // take half the state's columns, then half of w B.
+    constexpr int T = C::kBT;
+    constexpr int NR = kTok / (T / 8);
+    const bool does_b = !OUT || DP > 64 || warp < 8, does_x = OUT && (DP > 64 || warp >= 8);
     const int t = tid - 128, r0 = t >> 3;
+    const int q4 = warp & 3, row = q4 * 32 + lane, half = DP > 64 ? (warp - 4) >> 2 : 0;
+    const uint32_t la = uint32_t(q4 * 32) << 16;
     const uint64_t m1 = pair(-1.f, -1.f);
+    float* scr = reinterpret_cast<float*>(gb + C::kLo);  // free once the last update is done
     float w[NR], cf = 1.f;
     int nw = 0;  // tokens the weights are for
-    bool ok = true;
-    for (int i = 0; i < N; ++i) {
+    uint32_t ph = 0;
+    auto scale_b = [&](int i) -> bool {
       const int s = i % C::NS, n = tokens(i);
       if (n != nw || !OUT) {
 #pragma unroll
@@ -440,11 +468,11 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         nw = n;
         if (!OUT) cf *= ms->pw[n];
       }
-      if (!(ok = mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag))) break;
+      if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
       // the lo buffer's last reader is update i - NLO
-      if (i >= C::NLO && !(ok = mbar_wait(bar(ms->u_done[(i - C::NLO) & 1]), ((i - C::NLO) >> 1) & 1, abort_flag))) break;
-      if (OUT && !(ok = mbar_wait(bar(ms->s_full[i % C::SB]), (i / C::SB) & 1, abort_flag))) break;  // B has been read
-      if (OUT && DP > 64 && !(ok = mbar_wait(bar(ms->qx_done), i & 1, abort_flag))) break;           // so has X's image
+      if (i >= C::NLO && !mbar_wait(bar(ms->u_done[(i - C::NLO) & 1]), ((i - C::NLO) >> 1) & 1, abort_flag)) return false;
+      if (OUT && !mbar_wait(bar(ms->s_full[i % C::SB]), (i / C::SB) & 1, abort_flag)) return false;  // B has been read
+      if (OUT && DP > 64 && !mbar_wait(bar(ms->qx_done), i & 1, abort_flag)) return false;           // so has X's image
       uint8_t* hi = gb + s * C::kStageB + 16 * t;
       uint8_t* lo = gb + C::kLo + (i % C::NLO) * C::kOpB + 16 * t;
 #pragma unroll 1
@@ -481,90 +509,71 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms->bh_full[i & 1]));
-    }
-    if (!OUT && warp < 8) {
-      // the segment's state (thread = row, b's column)
-      const int row = tid - 128;
-      const uint32_t la = uint32_t((warp & 3) * 32) << 16;
-      uint32_t ph = 0;
-      ok = ok && mbar_wait(bar(ms->u_done[(N - 1) & 1]), ((N - 1) >> 1) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc_fence_after();
-        float* scr = reinterpret_cast<float*>(gb + C::kLo);  // free: the last update is done
-#pragma unroll 1
-        for (int x = 0; x < DP / 32; ++x) {
-          uint32_t v[32];
-          tmem_ld32(tmem + la + 32 * x, v);
-          tmem_wait_ld();
-          if (DP == 64 && !fold_lo(v, scr, row, ms, ph)) break;
-          store_state(x_out, v, x, row, d, DP, job.trans);
-        }
-      }
-    }
-  } else if (OUT && warp >= 8 && warp < 12) {
-    // ------------------------------------------------------------ state (thread = row of X, b's column)
-    const int q4 = warp & 3, row = q4 * 32 + lane;
-    const uint32_t la = uint32_t(q4 * 32) << 16;
-    const bool real = row < d;  // d <= 64: rows 64.. are the lo products', from zero
-    if (x_in) pdl_wait();  // the carried states are written by the kernel before
-    bool ok = true;
-    uint32_t ph = 0;
-    for (int i = 0; ok && i <= N; ++i) {
-      if (i > 0) {
-        if (!(ok = mbar_wait(bar(ms->u_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort_flag))) break;
-        tc_fence_after();
-      }
-      if (i == N && !x_out) break;
-      const float f = i < N ? ms->pw[tokens(i)] : 1.f;
+      return true;
+    };
+    // The image of X for chunk i and X scaled for its update
+    auto hand_on = [&](int i) {
+      const float f = ms->pw[tokens(i)];
       const uint64_t ff = pair(f, f);
-      float* scr = reinterpret_cast<float*>(gb + C::kLo);  // free once the last update is done
 #pragma unroll 1
-      for (int x = 0; x < DP / 32; ++x) {
+      for (int x = 2 * half; x < 2 * half + 2; ++x) {
         uint32_t v[32];
         if (i > 0) {
           tmem_ld32(tmem + la + 32 * x, v);
           tmem_wait_ld();
         } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0u;
-          if (x_in && real && job.trans) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * x + e < d) v[e] = __float_as_uint(x_in[(32 * x + e) * d + row]);
-          } else if (x_in && real) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              if (32 * x + e < d) *reinterpret_cast<uint4*>(v + e) = *reinterpret_cast<const uint4*>(x_in + row * d + 32 * x + e);
-          }
+          load_state(v, x_in, x, row, d, job.trans);
         }
-        if (i < N) {
-          if (DP > 64 || row < 64) {
-            uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
+        if (DP > 64 || row < 64) {
+          uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(img + ((((x & 1) * 4 + q) ^ (row & 7)) << 4)) =
-                  make_uint4(pack2(pair(v[8 * q], v[8 * q + 1])), pack2(pair(v[8 * q + 2], v[8 * q + 3])),
-                             pack2(pair(v[8 * q + 4], v[8 * q + 5])), pack2(pair(v[8 * q + 6], v[8 * q + 7])));
-          }
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(img + ((((x & 1) * 4 + q) ^ (row & 7)) << 4)) =
+                make_uint4(pack2(pair(v[8 * q], v[8 * q + 1])), pack2(pair(v[8 * q + 2], v[8 * q + 3])),
+                           pack2(pair(v[8 * q + 4], v[8 * q + 5])), pack2(pair(v[8 * q + 6], v[8 * q + 7])));
+        }
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) unpair(mul2(pair(v[e], v[e + 1]), ff), v[e], v[e + 1]);
-          tmem_st32(tmem + la + 32 * x, v);
+        for (int e = 0; e < 32; e += 2) unpair(mul2(pair(v[e], v[e + 1]), ff), v[e], v[e + 1]);
+        tmem_st32(tmem + la + 32 * x, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ms->x_full));  // the update may go ahead
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ms->img_full[i & 1]));
+    };
+    // X behind the last chunk, to memory
+    auto write_out = [&]() {
+#pragma unroll 1
+      for (int x = 2 * half; x < 2 * half + 2; ++x) {
+        uint32_t v[32];
+        if (N > 0) {
+          tmem_ld32(tmem + la + 32 * x, v);
+          tmem_wait_ld();
+          if (DP == 64 && !fold_lo(v, scr, row, ms, ph)) return;
         } else {
-          if (DP == 64 && !(ok = fold_lo(v, scr, row, ms, ph))) break;
-          store_state(x_out, v, x, row, d, DP, job.trans);
+          load_state(v, x_in, x, row, d, job.trans);
         }
+        store_state(x_out, v, x, row, d, DP, job.trans);
       }
-      if (i < N) {
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ms->x_full));  // the update may go ahead
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ms->img_full[i & 1]));
+    };
+    auto updated = [&](int i) -> bool {
+      const bool ok = mbar_wait(bar(ms->u_done[i & 1]), (i >> 1) & 1, abort_flag);
+      tc_fence_after();
+      return __all_sync(0xffffffffu, ok);
+    };
+    if (does_x && x_in) pdl_wait();  // the carried states are written by the kernel before
+    bool ok = true;
+    for (int i = 0; ok && i < N; ++i) {
+      if (does_x) {
+        if (i > 0 && !(ok = updated(i - 1))) break;
+        hand_on(i);
       }
+      if (does_b) ok = scale_b(i);
     }
+    if (ok && x_out && (does_x || (!OUT && (DP > 64 || warp < 8))) && (N <= 0 || updated(N - 1))) write_out();
   } else if (OUT && warp >= 12 && warp < 20) {
     // ------------------------------------------------------------ scores -> P (thread = row, half the columns)
     const int q4 = warp & 3, row = q4 * 32 + lane, half = (warp - 12) >> 2;
