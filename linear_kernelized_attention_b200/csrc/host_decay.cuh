@@ -124,14 +124,14 @@ int launch_decay_cc(dcy::Params p, int dtype_code, cudaStream_t st) {
   int rc = scratch_alloc(&ws, decay_cc_workspace(p.B, p.H, p.L, p.d, p.nstates), st);
   if (rc != FAVOR_OK) return rc;
   p.ws = static_cast<float*>(ws);
+  p.vec = dtype_code == 0 && p.d % 4 == 0;
+  for (int i = 0; i < p.nouts; ++i)
+    for (const View* v : {&p.o[i].a, &p.o[i].b, &p.o[i].c, &p.o[i].y})
+      if (v->sb % 4 != 0 || v->sh % 4 != 0 || v->st % 4 != 0) p.vec = 0;
   if (dtype_code == 0)
-    rc = p.d <= 32   ? launch_decay_cc_t<float, 32>(p, st)
-         : p.d <= 64 ? launch_decay_cc_t<float, 64>(p, st)
-                     : launch_decay_cc_t<float, 128>(p, st);
+    rc = p.d <= 64 ? launch_decay_cc_t<float, 64>(p, st) : launch_decay_cc_t<float, 128>(p, st);
   else
-    rc = p.d <= 32   ? launch_decay_cc_t<__nv_bfloat16, 32>(p, st)
-         : p.d <= 64 ? launch_decay_cc_t<__nv_bfloat16, 64>(p, st)
-                     : launch_decay_cc_t<__nv_bfloat16, 128>(p, st);
+    rc = p.d <= 64 ? launch_decay_cc_t<__nv_bfloat16, 64>(p, st) : launch_decay_cc_t<__nv_bfloat16, 128>(p, st);
   cudaFreeAsync(ws, st);
   return rc;
 }

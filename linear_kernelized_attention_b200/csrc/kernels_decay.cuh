@@ -63,6 +63,7 @@ struct Params {
   const int* lengths;      // [B] or null
   float* ws;               // [states][BH][nch][d * d]
   int nstates, nouts, B, H, L, d, nch;
+  int vec;  // fp32 rows and strides of whole 16-byte pieces
 };
 
 struct ScanParams {
@@ -90,23 +91,63 @@ __device__ __forceinline__ int seq_len(const int* lengths, int b, int L) {
   return lengths ? max(0, min(lengths[b], L)) : L;
 }
 
-// Rows row0 .. row0 + 63 of one head into dst[64][DP] as fp32; zero past n rows and d columns.
-template <typename T, int DP>
-__device__ __forceinline__ void load_tile(float* dst, const View& x, int b, int h, int row0, int n, int d) {
-  const T* src = static_cast<const T*>(x.p) + b * x.sb + h * x.sh + (long long)row0 * x.st;
-  for (int i = threadIdx.x; i < kChunk * DP; i += kThreads) {
-    const int r = i / DP, m = i % DP;
-    dst[i] = r < n && m < d ? to_f(src[r * x.st + m]) : 0.f;
-  }
+// Four consecutive elements as fp32, zeros past `left` of them.
+__device__ __forceinline__ float4 load4(const float* p, int left, bool vec) {
+  if (left <= 0) return make_float4(0.f, 0.f, 0.f, 0.f);
+  if (vec) return *reinterpret_cast<const float4*>(p);
+  return make_float4(p[0], left > 1 ? p[1] : 0.f, left > 2 ? p[2] : 0.f, left > 3 ? p[3] : 0.f);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p, int left, bool) {
+  return make_float4(left > 0 ? to_f(p[0]) : 0.f, left > 1 ? to_f(p[1]) : 0.f, left > 2 ? to_f(p[2]) : 0.f,
+                     left > 3 ? to_f(p[3]) : 0.f);
 }
 
-// ws[state][bh][chunk][m][n] = sum_r w_r b_r[m] c_r[n]. Grid: states x BH x chunks, chunk fastest.
+// A thread's pieces of 64 rows x DP columns (piece i: row i / (DP / 4), columns 4 (i % (DP / 4)) ..): all in
+// flight together, then into shared memory.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) k_chunk_update(const Params p) {
+struct Rows {
+  static constexpr int NP = kChunk * DP / 4 / kThreads;
+  float4 v[NP];
+  __device__ __forceinline__ void load(const View& x, int b, int h, int row0, int n, int d, bool vec) {
+    const T* src = static_cast<const T*>(x.p) + b * x.sb + h * x.sh + (long long)row0 * x.st;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = threadIdx.x + k * kThreads, r = i / (DP / 4), m = 4 * (i % (DP / 4));
+      v[k] = load4(src + (r < n ? r * x.st : 0) + m, r < n ? d - m : 0, vec);
+    }
+  }
+  // rows `stride` floats apart; scale: a factor per row, or null
+  __device__ __forceinline__ void store(float* dst, int stride, const float* scale) const {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = threadIdx.x + k * kThreads, r = i / (DP / 4), m = 4 * (i % (DP / 4));
+      const float w = scale ? scale[r] : 1.f;
+      *reinterpret_cast<float4*>(dst + r * stride + m) = make_float4(v[k].x * w, v[k].y * w, v[k].z * w, v[k].w * w);
+    }
+  }
+};
+
+__device__ __forceinline__ void fma4(float (&acc)[4], float x, const float4& y) {
+  acc[0] = fmaf(x, y.x, acc[0]);
+  acc[1] = fmaf(x, y.y, acc[1]);
+  acc[2] = fmaf(x, y.z, acc[2]);
+  acc[3] = fmaf(x, y.w, acc[3]);
+}
+__device__ __forceinline__ float dot4(const float4& x, const float4& y, float s) {
+  return fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, fmaf(x.x, y.x, s))));
+}
+__device__ __forceinline__ float part(const float4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
+
+// ws[state][bh][chunk][m][n] = sum_r w_r b_r[m] c_r[n]. Grid: states x BH x chunks, chunk fastest.
+// A thread sums tiles of 4 x 4 elements: 16 fma on two 16-byte reads a token.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) k_chunk_update(const __grid_constant__ Params p) {
+  constexpr int K = DP / 64;
   extern __shared__ float sm[];
   pdl_launch_dependents();
   float* sb = sm;                 // [kChunk][DP], rows scaled by w_r
   float* sc = sm + kChunk * DP;   // [kChunk][DP]
+  float* sw = sc + kChunk * DP;   // w_r
   const int ch = blockIdx.x % p.nch, q = blockIdx.x / p.nch;
   const int bh = q % (p.B * p.H), js = q / (p.B * p.H);
   const int b = bh / p.H, h = bh % p.H;
@@ -114,40 +155,62 @@ __global__ void __launch_bounds__(kThreads) k_chunk_update(const Params p) {
   const int len = seq_len(p.lengths, b, p.L);
   const int row0 = ch * kChunk, n = min(kChunk, len - row0);
   if (n <= 0) return;
-  load_tile<T, DP>(sb, job.b, b, h, row0, n, p.d);
-  load_tile<T, DP>(sc, job.c, b, h, row0, n, p.d);
+  Rows<T, DP> xb, xc;
+  xb.load(job.b, b, h, row0, n, p.d, p.vec);
+  xc.load(job.c, b, h, row0, n, p.d, p.vec);
+  if (threadIdx.x < kChunk)
+    sw[threadIdx.x] =
+        threadIdx.x < n ? (float)decay_pow(p.log_decay[h], job.reverse ? threadIdx.x + 1 : n - 1 - threadIdx.x) : 0.f;
   __syncthreads();
-  const float g = p.log_decay[h];
-  {
-    const int r = threadIdx.x >> 2;  // four threads scale one row
-    if (r < n) {
-      const float w = (float)decay_pow(g, job.reverse ? r + 1 : n - 1 - r);
-      for (int m = threadIdx.x & 3; m < DP; m += 4) sb[r * DP + m] *= w;
-    }
-  }
+  xb.store(sb, DP, sw);
+  xc.store(sc, DP, nullptr);
   __syncthreads();
-  constexpr int R = DP / 16;
-  const int m0 = (threadIdx.x >> 4) * R, n0 = (threadIdx.x & 15) * R;
-  float acc[R][R];
+  const int m0 = 4 * (threadIdx.x >> 4), n0 = 4 * (threadIdx.x & 15);
+  if (m0 >= p.d) return;
+  float acc[K][4][K][4];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int l = 0; l < K; ++l)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[k][i][l][j] = 0.f;
+#pragma unroll 4
   for (int r = 0; r < n; ++r) {
-    float x[R], y[R];
+    float4 x[K], y[K];
 #pragma unroll
-    for (int i = 0; i < R; ++i) x[i] = sb[r * DP + m0 + i], y[i] = sc[r * DP + n0 + i];
+    for (int k = 0; k < K; ++k) {
+      x[k] = *reinterpret_cast<const float4*>(sb + r * DP + m0 + 64 * k);
+      y[k] = *reinterpret_cast<const float4*>(sc + r * DP + n0 + 64 * k);
+    }
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int j = 0; j < R; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int l = 0; l < K; ++l) fma4(acc[k][i][l], part(x[k], i), y[l]);
   }
   float* out = p.ws + ((long long)q * p.nch + ch) * p.d * p.d;
+  const bool v4 = p.d % 4 == 0;
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-      if (m0 + i < p.d && n0 + j < p.d) out[(m0 + i) * p.d + n0 + j] = acc[i][j];
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int l = 0; l < K; ++l) {
+        const int m = m0 + 64 * k + i, c = n0 + 64 * l;
+        if (m < p.d && c < p.d) {
+          const float* a = acc[k][i][l];
+          if (v4) {
+            *reinterpret_cast<float4*>(out + m * p.d + c) = make_float4(a[0], a[1], a[2], a[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (c + j < p.d) out[m * p.d + c + j] = a[j];
+          }
+        }
+      }
 }
 
 // Each segment's update (p.seg tokens; a chunk is one) replaced by the state it is handed; the
@@ -187,57 +250,66 @@ static __global__ void __launch_bounds__(kThreads) k_chunk_scan(const __grid_con
   if (p.out[js]) p.out[js][(long long)bh * dd + el] = (float)x;
 }
 
-// y rows of one chunk. Grid: outs x BH x chunks, chunk fastest.
+// y rows of one chunk. Grid: outs x BH x chunks, chunk fastest. A thread sums 4 rows by 4 (or twice 4)
+// columns of each product, 64 fma on eight 16-byte reads; the score rows overwrite b. Operands arrive
+// while the scan runs; the carried state follows it.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
-  constexpr int PS = kChunk + 1;  // row stride of the weighted scores (no bank conflicts down a column)
-  constexpr int AS = DP + 1;
-  constexpr int XR = 32;          // state rows staged at a time
+__global__ void __launch_bounds__(kThreads) k_chunk_out(const __grid_constant__ Params p) {
+  constexpr int AS = DP + 4;      // row stride: 16-byte pieces, eight rows on distinct banks
+  constexpr int PS = kChunk + 4;
+  constexpr int K = DP / 64;
   extern __shared__ float sm[];
   float* sa = sm;                       // [kChunk][AS]
-  float* sb = sa + kChunk * AS;         // [kChunk][AS], then state rows [XR][DP]
-  float* sc = sb + kChunk * AS;         // [kChunk][DP]
-  float* sp = sc + kChunk * DP;         // [kChunk][PS]
-  float* pw = sp + kChunk * PS;         // lambda^0 .. lambda^64
+  float* sb = sa + kChunk * AS;         // [kChunk][AS], then the weighted scores [kChunk][PS]
+  float* sc = sb + kChunk * AS;         // [kChunk][AS]
+  float* sx = sc + kChunk * AS;         // [DP][AS], X or its transpose
+  float* pw = sx + DP * AS;             // lambda^0 .. lambda^64
+  float* sp = sb;
+  pdl_launch_dependents();
   const int ch = blockIdx.x % p.nch, q = blockIdx.x / p.nch;
   const int bh = q % (p.B * p.H), jo = q / (p.B * p.H);
   const int b = bh / p.H, h = bh % p.H;
   const OutJob& job = p.o[jo];
   const int len = seq_len(p.lengths, b, p.L);
-  const int row0 = ch * kChunk, n = min(kChunk, len - row0);
-  pdl_wait();
-  if (n <= 0) return;
+  const int row0 = ch * kChunk, n = min(kChunk, len - row0), d = p.d;
+  if (n <= 0) {
+    pdl_wait();
+    return;
+  }
   const int rev = job.reverse;
-  auto load_padded = [&](float* dst, const View& x) {
-    const T* src = static_cast<const T*>(x.p) + b * x.sb + h * x.sh + (long long)row0 * x.st;
-    for (int i = threadIdx.x; i < kChunk * DP; i += kThreads) {
-      const int r = i / DP, m = i % DP;
-      dst[r * AS + m] = r < n && m < p.d ? to_f(src[r * x.st + m]) : 0.f;
-    }
-  };
-  load_padded(sa, job.a);
-  load_padded(sb, job.b);
-  load_tile<T, DP>(sc, job.c, b, h, row0, n, p.d);
-  if (threadIdx.x <= kChunk) pw[threadIdx.x] = (float)decay_pow(p.log_decay[h], threadIdx.x);
+  {
+    Rows<T, DP> xa, xb, xc;
+    xa.load(job.a, b, h, row0, n, d, p.vec);
+    xb.load(job.b, b, h, row0, n, d, p.vec);
+    xc.load(job.c, b, h, row0, n, d, p.vec);
+    if (threadIdx.x <= kChunk) pw[threadIdx.x] = (float)decay_pow(p.log_decay[h], threadIdx.x);
+    xa.store(sa, AS, nullptr);
+    xb.store(sb, AS, nullptr);
+    xc.store(sc, AS, nullptr);
+  }
   __syncthreads();
 
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int i0 = 4 * ty;
+  const int i0 = 4 * ty, d4 = (d + 3) / 4 * 4;
   {  // scores of rows 4 ty .. + 3 and columns tx, tx + 16, ...
     float s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-    for (int m = 0; m < p.d; ++m) {
-      float x[4], y[4];
+    for (int m = 0; m < d4; m += 4) {
+      float4 x[4], y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = sa[(i0 + i) * AS + m], y[i] = sb[(tx + 16 * i) * AS + m];
+      for (int i = 0; i < 4; ++i) {
+        x[i] = *reinterpret_cast<const float4*>(sa + (i0 + i) * AS + m);
+        y[i] = *reinterpret_cast<const float4*>(sb + (tx + 16 * i) * AS + m);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = fmaf(x[i], y[j], s[i][j]);
+        for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
     }
+    __syncthreads();  // b is read
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -246,59 +318,58 @@ __global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
         sp[(i0 + i) * PS + tx + 16 * j] = gap >= 0 ? s[i][j] * pw[gap] : 0.f;
       }
   }
+  {  // the carried state, zeros past d; columns of X are X's own unless transposed
+    pdl_wait();
+    const float* X = p.ws + (((long long)job.state * p.B * p.H + bh) * p.nch + ch) * d * d;
+    const bool v4 = d % 4 == 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < DP * DP / 4; i += kThreads) {
+      const int r = i / (DP / 4), c = 4 * (i % (DP / 4));
+      const float4 v = load4(X + (r < d ? r * d : 0) + c, r < d ? d - c : 0, v4);
+      if (job.trans) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sx[(c + e) * AS + r] = part(v, e);
+      } else {
+        *reinterpret_cast<float4*>(sx + r * AS + c) = v;
+      }
+    }
+  }
   __syncthreads();
 
-  constexpr int R = DP / 16;
-  float acc[4][R];
+  float acc[4][K][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
-  // the carried state: acc = a X
-  const float* X = p.ws + (((long long)job.state * p.B * p.H + bh) * p.nch + ch) * p.d * p.d;
-  float* sx = sb;
-  for (int m0 = 0; m0 < p.d; m0 += XR) {
-    const int nm = min(XR, p.d - m0);
-    for (int i = threadIdx.x; i < XR * DP; i += kThreads) {
-      int m, c;
-      if (job.trans) m = i % XR, c = i / XR; else m = i / DP, c = i % DP;
-      const bool ok = m < nm && c < p.d;
-      sx[m * DP + c] = ok ? (job.trans ? X[c * p.d + m0 + m] : X[(m0 + m) * p.d + c]) : 0.f;
-    }
-    __syncthreads();
-    for (int m = 0; m < nm; ++m) {
-      float x[4];
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = sa[(i0 + i) * AS + m0 + m];
+      for (int j = 0; j < 4; ++j) acc[i][k][j] = 0.f;
+  // rows of `x` times rows m .. m + 3 of `y`
+  auto step = [&](const float* x, int xs, const float* y) {
+    float4 a[4];
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const float y = sx[m * DP + tx + 16 * j];
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(x + i * xs);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][j] = fmaf(x[i], y, acc[i][j]);
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(y + e * AS + 4 * tx + 64 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fma4(acc[i][k], part(a[i], e), v);
       }
-    }
-    __syncthreads();
-  }
+  };
+  for (int m = 0; m < d4; m += 4) step(sa + i0 * AS + m, AS, sx + m * AS);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i0 + i;
     const float w = r < n ? pw[rev ? n - 1 - r : r + 1] : 0.f;
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[i][j] *= w;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][k][j] *= w;
   }
   // the chunk itself: every key all four rows see, then the diagonal 4 x 4 block element by element
-  const int lo = rev ? i0 + 4 : 0, hi = rev ? n : i0;
-  for (int r = lo; r < hi; ++r) {
-    float x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = sp[(i0 + i) * PS + r];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const float y = sc[r * DP + tx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i][j] = fmaf(x[i], y, acc[i][j]);
-    }
-  }
+  const int lo = rev ? i0 + 4 : 0, hi = rev ? (n + 3) / 4 * 4 : i0;
+  for (int r = lo; r < hi; r += 4) step(sp + i0 * PS + r, PS, sc + r * AS);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -306,22 +377,31 @@ __global__ void __launch_bounds__(kThreads) k_chunk_out(const Params p) {
       if ((rev ? r >= i : r <= i) && i0 + r < n) {
         const float x = sp[(i0 + i) * PS + i0 + r];
 #pragma unroll
-        for (int j = 0; j < R; ++j) acc[i][j] = fmaf(x, sc[(i0 + r) * DP + tx + 16 * j], acc[i][j]);
+        for (int k = 0; k < K; ++k)
+          fma4(acc[i][k], x, *reinterpret_cast<const float4*>(sc + (i0 + r) * AS + 4 * tx + 64 * k));
       }
   T* y = static_cast<T*>(job.y.p) + b * job.y.sb + h * job.y.sh;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (i0 + i >= n) continue;
+    T* yr = y + (long long)(row0 + i0 + i) * job.y.st;
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-      if (tx + 16 * j < p.d) from_f(y[(long long)(row0 + i0 + i) * job.y.st + tx + 16 * j], acc[i][j]);
+    for (int k = 0; k < K; ++k) {
+      const int c = 4 * tx + 64 * k;
+      if (c >= d) continue;
+      if (p.vec && sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(yr + c) = make_float4(acc[i][k][0], acc[i][k][1], acc[i][k][2], acc[i][k][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < d) from_f(yr[c + j], acc[i][k][j]);
+      }
+    }
   }
 }
 
-constexpr int update_smem(int dp) { return 2 * kChunk * dp * 4; }
-constexpr int out_smem(int dp) {
-  return (2 * kChunk * (dp + 1) + kChunk * dp + kChunk * (kChunk + 1) + kChunk + 1) * 4;
-}
+constexpr int update_smem(int dp) { return (2 * kChunk * dp + kChunk) * 4; }
+constexpr int out_smem(int dp) { return (3 * kChunk * (dp + 4) + dp * (dp + 4) + kChunk + 4) * 4; }
 
 }  // namespace dcy
 }  // namespace favor
