@@ -3,6 +3,7 @@
 #pragma once
 #include <cmath>
 
+#include "kernel_decay_state.cuh"
 #include "kernel_decay_step.cuh"
 #include "kernel_decay_tc.cuh"
 #include "kernel_rotary.cuh"
@@ -137,28 +138,29 @@ int launch_decay_cc(dcy::Params p, int dtype_code, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ tensor-core route
-// How a call's walk is cut: chunks per segment, segments. `scan`: segment states, the scan and the
-// walk (three launches); else one walk per head from the carried-in state.
+// How a call's walk is cut: chunks per segment, segments. `scan` (several segments): segment states,
+// their scan and the walk, three launches; else one walk per head from the carried-in state, and beside it
+// the states a caller wants back.
 struct WalkPlan {
   int cps, nseg;
   bool scan;
 };
 
-// The number of segments with the least estimated time, in chunks of walking: a CTA's start and
-// end cost about two chunks, a chunk of the states alone about 0.6 of a chunk of the walk, the two
-// further launches about three.
-WalkPlan plan_walk(int BH, int L, int nstates, int njobs, bool force_scan) {
+// The number of segments with the least estimated time, in microseconds. Measured: a block of the walk takes
+// 3 and 1.6 (d <= 64) or 2.95 a chunk, one of the states alone 3 and 0.75 or 1.4 a chunk, the scan and the
+// gaps of two further launches 6 and a hundredth a segment.
+WalkPlan plan_walk(int BH, int L, int d, int nstates, int njobs) {
   const int nch = (int)(((long long)L + dtc::kTok - 1) / dtc::kTok), sms = sm_count();
+  const double tw = d <= 64 ? 1.6 : 2.95, ts = d <= 64 ? 0.75 : 1.4;
   auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
   WalkPlan best{};
   double cost = 1e300;
   for (int k = 1; k <= std::min(nch, 1024); ++k) {
     const int cps = (nch + k - 1) / k, nseg = (nch + cps - 1) / cps;
     if (nseg != k) continue;  // as many segments as the chunks per segment need
-    const bool scan = k > 1 || force_scan;
-    double t = waves((long long)BH * njobs * nseg) * (cps + 2.0);
-    if (scan) t += waves((long long)BH * nstates * nseg) * (0.6 * cps + 2.0) + 3.0 + 0.05 * nseg;
-    if (t < cost) cost = t, best = WalkPlan{cps, nseg, scan};
+    double t = waves((long long)BH * njobs * nseg) * (tw * cps + 3.0);
+    if (k > 1) t += waves((long long)BH * nstates * nseg) * (ts * cps + 3.0) + 6.0 + 0.01 * nseg;
+    if (t < cost) cost = t, best = WalkPlan{cps, nseg, k > 1};
     if ((long long)BH * nseg > 8ll * sms) break;
   }
   return best;
@@ -202,53 +204,58 @@ size_t walk_workspace(const WalkPlan& pl, int BH, int d, int nstates) {
   return pl.scan ? (size_t)nstates * BH * pl.nseg * d * d * sizeof(float) : 0;
 }
 
-template <int DP>
-int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaStream_t st) {
-  dtc::Params tp{};
-  int nm = 0;
-  const void* seen[4];
-  long long sst[4][3];
-  // operands by pointer and strides: forward q, k, v; backward q, k, v, dout
-  auto operand = [&](const View& v) -> int {
-    for (int i = 0; i < nm; ++i)
-      if (seen[i] == v.p && sst[i][0] == v.sb && sst[i][1] == v.sh && sst[i][2] == v.st) return i;
-    if (nm == 4 || !make_map_view(&tp.m[nm], &tp.bm[nm], &tp.hm[nm], v, p.B, p.H, p.L, p.d, false))
-      return -1;
-    seen[nm] = v.p;
-    sst[nm][0] = v.sb, sst[nm][1] = v.sh, sst[nm][2] = v.st;
-    return nm++;
-  };
-  tp.log_decay = p.log_decay;
-  tp.lengths = p.lengths;
-  tp.B = p.B, tp.H = p.H, tp.L = p.L, tp.d = p.d, tp.nseg = pl.nseg, tp.cps = pl.cps;
-  const long long tasks = (long long)p.B * p.H * pl.nseg;
-  if (tasks * 3 > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
-  if (pl.scan) {
-    using C = dtc::Cfg<DP, false>;
-    auto ks = dtc::k_decay_walk<DP, false>;
-    if (ensure_smem_attr(reinterpret_cast<const void*>(ks), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
-    tp.ws = ws;
-    tp.njobs = p.nstates;
-    for (int i = 0; i < p.nstates; ++i) {
-      tp.j[i].b = operand(p.s[i].b);
-      tp.j[i].c = operand(p.s[i].c);
-      if (tp.j[i].b < 0 || tp.j[i].c < 0) return FAVOR_ERR_CUDA;
-      tp.j[i].state = i;
-      tp.j[i].reverse = p.s[i].reverse;
-    }
-    int rc = launch_with<dtc::Params>(ks, tasks * p.nstates, C::kThreads, C::kSmem, st, false, tp);
-    if (rc == FAVOR_OK) rc = launch_scan(p, ws, pl.nseg, pl.cps * dtc::kTok, st);
-    if (rc != FAVOR_OK) return rc;
+// Tensor maps of a call's operands, by pointer and strides: forward q, k, v; backward q, k, v, dout.
+struct OperandMaps {
+  CUtensorMap m[4];
+  int bm[4], hm[4], n = 0;
+  View seen[4];
+  int add(const View& v, const dcy::Params& p) {
+    for (int i = 0; i < n; ++i)
+      if (seen[i].p == v.p && seen[i].sb == v.sb && seen[i].sh == v.sh && seen[i].st == v.st) return i;
+    if (n == 4 || !make_map_view(&m[n], &bm[n], &hm[n], v, p.B, p.H, p.L, p.d, false)) return -1;
+    seen[n] = v;
+    return n++;
   }
-  using C = dtc::Cfg<DP, true>;
-  auto kw = dtc::k_decay_walk<DP, true>;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(kw), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
+};
+
+// The states in p.s that have a use: every segment's (ws), or the whole sequences' written to their `out`.
+template <int DP>
+int launch_states(const dcy::Params& p, OperandMaps& om, float* ws, int nseg, int cps, bool beside, cudaStream_t st) {
+  using C = dst::Cfg<DP>;
+  dst::Params sp{};
+  for (int i = 0; i < p.nstates; ++i) {
+    if (!ws && !p.s[i].out) continue;
+    dst::Job& j = sp.j[sp.njobs++];
+    j.b = om.add(p.s[i].b, p);
+    j.c = om.add(p.s[i].c, p);
+    if (j.b < 0 || j.c < 0) return FAVOR_ERR_CUDA;
+    j.reverse = p.s[i].reverse;
+    j.in = p.s[i].in;
+    j.out = p.s[i].out;
+  }
+  if (!sp.njobs) return FAVOR_OK;
+  std::copy(om.m, om.m + 4, sp.m);
+  std::copy(om.bm, om.bm + 4, sp.bm);
+  std::copy(om.hm, om.hm + 4, sp.hm);
+  sp.ws = ws;
+  sp.log_decay = p.log_decay;
+  sp.lengths = p.lengths;
+  sp.B = p.B, sp.H = p.H, sp.L = p.L, sp.d = p.d, sp.nseg = nseg, sp.cps = cps;
+  auto k = dst::k_decay_state<DP>;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(k), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
+  return launch_with<dst::Params>(k, (long long)p.B * p.H * nseg * sp.njobs, C::kThreads, C::kSmem, st, beside, sp);
+}
+
+template <int DP>
+int launch_walk(const dcy::Params& p, OperandMaps& om, const float* ws, const WalkPlan& pl, cudaStream_t st) {
+  using C = dtc::Cfg<DP>;
+  dtc::Params tp{};
   tp.njobs = p.nouts;
   for (int i = 0; i < p.nouts; ++i) {
     dtc::Job& j = tp.j[i];
-    j.a = operand(p.o[i].a);
-    j.b = operand(p.o[i].b);
-    j.c = operand(p.o[i].c);
+    j.a = om.add(p.o[i].a, p);
+    j.b = om.add(p.o[i].b, p);
+    j.c = om.add(p.o[i].c, p);
     if (j.a < 0 || j.b < 0 || j.c < 0) return FAVOR_ERR_CUDA;
     j.state = p.o[i].state;
     j.trans = p.o[i].trans;
@@ -256,16 +263,40 @@ int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaS
     j.va = p.o[i].a, j.vb = p.o[i].b, j.vc = p.o[i].c, j.y = p.o[i].y;
     int bm, hm;
     if (!make_map_view(&tp.my[i], &bm, &hm, j.y, p.B, p.H, p.L, p.d, true)) return FAVOR_ERR_CUDA;
-    j.final = !pl.scan && (i == 0 || p.o[i].state != p.o[i - 1].state);
   }
-  for (int i = 0; i < p.nstates; ++i) tp.in[i] = p.s[i].in, tp.out[i] = p.s[i].out;
-  return launch_with<dtc::Params>(kw, tasks * p.nouts, C::kThreads, C::kSmem, st, pl.scan, tp);
+  std::copy(om.m, om.m + 4, tp.m);
+  std::copy(om.bm, om.bm + 4, tp.bm);
+  std::copy(om.hm, om.hm + 4, tp.hm);
+  for (int i = 0; i < p.nstates; ++i) tp.in[i] = p.s[i].in;
+  tp.ws = ws;
+  tp.log_decay = p.log_decay;
+  tp.lengths = p.lengths;
+  tp.B = p.B, tp.H = p.H, tp.L = p.L, tp.d = p.d, tp.nseg = pl.nseg, tp.cps = pl.cps;
+  auto k = dtc::k_decay_walk<DP>;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(k), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
+  return launch_with<dtc::Params>(k, (long long)p.B * p.H * pl.nseg * p.nouts, C::kThreads, C::kSmem, st, pl.scan, tp);
+}
+
+template <int DP>
+int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaStream_t st) {
+  if ((long long)p.B * p.H * pl.nseg * 3 > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
+  OperandMaps om;
+  int rc = FAVOR_OK;
+  if (pl.scan) {
+    rc = launch_states<DP>(p, om, ws, pl.nseg, pl.cps, false, st);
+    if (rc == FAVOR_OK) rc = launch_scan(p, ws, pl.nseg, pl.cps * dtc::kTok, st);
+    return rc == FAVOR_OK ? launch_walk<DP>(p, om, ws, pl, st) : rc;
+  }
+  rc = launch_walk<DP>(p, om, nullptr, pl, st);
+  if (rc != FAVOR_OK) return rc;
+  // the whole sequences' states: beside the walk, or after it where they overwrite what it reads
+  bool beside = true;
+  for (int i = 0; i < p.nstates; ++i) beside = beside && !(p.s[i].out && p.s[i].out == p.s[i].in);
+  return launch_states<DP>(p, om, nullptr, 1, pl.cps, beside, st);
 }
 
 int launch_decay_tc(const dcy::Params& p, cudaStream_t st) {
-  // two jobs of the backward pass read dstate_out: in place it goes through the scan
-  const bool in_place = p.nouts > 1 && p.s[1].in && p.s[1].in == p.s[1].out;
-  const WalkPlan pl = plan_walk(p.B * p.H, p.L, p.nstates, p.nouts, in_place);
+  const WalkPlan pl = plan_walk(p.B * p.H, p.L, p.d, p.nstates, p.nouts);
   void* ws = nullptr;
   int rc = scratch_alloc(&ws, walk_workspace(pl, p.B * p.H, p.d, p.nstates), st);
   if (rc != FAVOR_OK) return rc;
@@ -336,7 +367,7 @@ size_t favor_decay_workspace_bytes(int B, int H, int L, int d, int dtype_code, i
   if (check_decay_sizes(B, H, L, d, dtype_code) != FAVOR_OK) return 0;
   const int ns = backward ? 2 : 1;
   if (dtype_code == 1 && d % 8 == 0)
-    return walk_workspace(plan_walk(B * H, L, ns, backward ? 3 : 1, false), B * H, d, ns);
+    return walk_workspace(plan_walk(B * H, L, d, ns, backward ? 3 : 1), B * H, d, ns);
   return decay_cc_workspace(B, H, L, d, ns);
 }
 

@@ -1,0 +1,320 @@
+// kernel_decay_state.cuh - the states of linear attention with a decay, to fp32 accuracy, on sm_100a
+// tensor cores.
+//
+// What it computes, for a segment of one head: X = sum_r w_r b_r c_r^T over the segment's tokens, w_r =
+// lambda^(tokens of the segment beyond r in the state's direction). As the only segment of a sequence it
+// adds lambda^len of the state carried in: state_out, or dstate_in.
+//
+// Precision. The caller gets X in fp32, so three things that the bf16 rows of kernel_decay_tc.cuh do
+// without are done here. w b is fed to the MMAs as three bf16 terms, hi + mid + lo, each the rounding of
+// what the ones before leave: 2^-26 of a product. Each 128-token chunk is summed from zero and added to
+// running sums in registers with fp32's own rounding: tensor cores truncate every accumulation, which
+// over a whole segment pulls a slowly decaying state towards zero (measured at 57 chunks and lambda^128
+// near 1: 1.4e-5 of the state's norm, against 4e-7 as it is). hi and the smaller terms have accumulators of
+// their own, so the large sums are truncated eight times a chunk, no more.
+//
+// Chunks are taken against the state's direction, so that a chunk's factor, the decay over the tokens
+// beyond it, grows from 1 by one product (in double) a chunk, and nothing is ever rescaled.
+//
+// Reading b and c bounds it: 32 KB a chunk and head at d = 64.
+//
+// Warps: 0 TMA; 1 TMEM allocation and MMAs; 4-11 the three terms of w b (hi in place, mid and lo beside
+// it); 12-15 (d <= 64) or 12-19 the running sums, thread = row of X (b's column).
+// d <= 64: [hi; mid] as the 128 rows of one operand, [lo; mid] as another whose second half is unused.
+#pragma once
+#include "kernel_decay_tc.cuh"
+
+namespace favor {
+namespace dst {
+
+using dtc::kAtomB;
+using dtc::kTok;
+
+struct Job {
+  int b, c;  // operands (indices into Params::m)
+  int reverse;
+  const float* in;  // one segment only: carried in (null: zeros)
+  float* out;       // one segment only
+};
+
+struct Params {
+  CUtensorMap m[4];
+  int bm[4], hm[4];  // 0 where an operand repeats over batch entries or heads
+  Job j[2];
+  float* ws;         // several segments: [states][BH][nseg][d * d]
+  const float* log_decay;
+  const int* lengths;
+  int njobs, B, H, L, d, nseg, cps;  // chunks per segment
+};
+
+template <int DP>
+struct Cfg {
+  static constexpr int NB = DP / 64;
+  static constexpr int kOpB = NB * kAtomB;
+  static constexpr int kStageB = 2 * kOpB;  // b, c
+  static constexpr int NS = DP == 64 ? 4 : 2;
+  static constexpr int NT = DP == 64 ? 2 : 1;       // buffers of (lo, mid)
+  static constexpr int kTerms = NS * kStageB;
+  static constexpr int kMisc = kTerms + NT * 2 * kOpB;
+  static constexpr int kSmem = kMisc + 2048 + 1024;
+  static constexpr int kThreads = DP == 64 ? 512 : 640;
+  static constexpr uint32_t kAcc = 2 * DP;          // columns of one chunk's accumulators: hi (and mid), the rest
+  static constexpr uint32_t kCols = 2 * kAcc;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Misc {
+  int abort_flag;
+  uint32_t tmem_base;
+  float pw[132];  // lambda^0 .. lambda^128
+  uint64_t full[4], empty[4], t_full[2], done[2], d_free[2], sync, drain;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __grid_constant__ Params p) {
+  using C = Cfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gb = smem_raw + (base - raw);
+  Misc* ms = reinterpret_cast<Misc*>(gb + C::kMisc);
+  volatile int* abort_flag = &ms->abort_flag;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int jid = blockIdx.x % p.njobs;
+  const int seg = (blockIdx.x / p.njobs) % p.nseg;
+  const int bh = blockIdx.x / p.njobs / p.nseg;
+  const int b = bh / p.H, h = bh % p.H;
+  const Job& job = p.j[jid];
+  const int rev = job.reverse, d = p.d;
+  const int len = dcy::seq_len(p.lengths, b, p.L);
+  const int nch = (int)(((long long)len + kTok - 1) / kTok);
+  const int c0 = seg * p.cps, c1 = min(nch, c0 + p.cps);
+  const int N = max(0, c1 - c0);
+  if (N == 0 && p.ws) {  // a segment behind the sequence's end
+    pdl_launch_dependents();
+    pdl_wait();
+    return;
+  }
+  auto chunk = [&](int i) { return rev ? c0 + i : c1 - 1 - i; };
+  auto tokens = [&](int i) { return min(kTok, len - chunk(i) * kTok); };
+  auto load = [&](int i) {  // one lane: chunk i into its stage
+    const int s = i % C::NS, row = chunk(i) * kTok;
+    const int op[2] = {job.b, job.c};
+    mbar_arrive_expect_tx(bar(ms->full[s]), C::kStageB);
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int x = 0; x < C::NB; ++x)
+        dtc::tma_load_4d(base + s * C::kStageB + o * C::kOpB + x * kAtomB, &p.m[op[o]], bar(ms->full[s]), 64 * x, row,
+                         h * p.hm[op[o]], b * p.bm[op[o]]);
+  };
+  if (tid == 0) {
+    ms->abort_flag = 0;
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(bar(ms->full[s]), 1);
+      mbar_init(bar(ms->empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(ms->t_full[s]), 8);
+      mbar_init(bar(ms->done[s]), 1);
+      mbar_init(bar(ms->d_free[s]), DP / 16);
+    }
+    mbar_init(bar(ms->sync), 128);
+    mbar_init(bar(ms->drain), 1);
+    fence_mbar_init();
+    for (int i = 0; i < min(N, C::NS); ++i) load(i);  // in flight while the block sets up
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ms->tmem_base), C::kCols);
+    tmem_relinquish();
+  }
+  if (tid >= 96 && tid <= 96 + kTok) ms->pw[tid - 96] = (float)dcy::decay_pow(p.log_decay[h], tid - 96);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ms->tmem_base, 0);
+
+  if (warp == 0) {
+    const bool leader = elect_one();
+    int issued = min(N, C::NS);
+    for (int i = issued; i < N; ++i) {
+      if (!mbar_wait(bar(ms->empty[i % C::NS]), ((i / C::NS) - 1) & 1, abort_flag)) break;
+      if (leader) load(i);
+      issued = i + 1;
+      __syncwarp();
+    }
+    if (*abort_flag)  // let the copies already issued land before the CTA can exit
+      for (int i = max(0, issued - C::NS); i < issued; ++i)
+        mbar_wait(bar(ms->full[i % C::NS]), (i / C::NS) & 1, nullptr, kWaitLimitCycles / 8);
+    __syncwarp();
+  } else if (warp == 1) {
+    // straight-line for the whole warp, as in kernel_decay_tc.cuh
+    const uint32_t lead = elect_one();
+    constexpr uint32_t id_u = idesc_f16(128, DP, 1, 1, 1, 1);
+    constexpr uint64_t kRows16 = (16 * 128) >> 4;
+    for (int i = 0; i < N; ++i) {
+      const int s = i % C::NS;
+      mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
+      mbar_wait(bar(ms->t_full[i & 1]), (i >> 1) & 1, abort_flag);
+      if (i >= 2) mbar_wait(bar(ms->d_free[i & 1]), ((i >> 1) - 1) & 1, abort_flag);
+      tc_fence_after();
+      const uint32_t hi = base + s * C::kStageB, lo = base + C::kTerms + (i % C::NT) * 2 * C::kOpB, mid = lo + C::kOpB;
+      const uint32_t acc = tmem + (i & 1) * C::kAcc;
+      const uint64_t dc = sdesc_sw128(hi + C::kOpB, kAtomB, 1024);
+      const uint64_t dh = sdesc_sw128(hi, DP == 64 ? mid - hi : kAtomB, 1024);
+      const uint64_t dl = sdesc_sw128(lo, kAtomB, 1024);  // d <= 64: mid is its second half
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        dtc::mma_ss_if(lead, acc, dh + kk * kRows16, dc + kk * kRows16, id_u, kk > 0 ? 1u : 0u);
+      if (DP > 64) {
+        const uint64_t dm = sdesc_sw128(mid, kAtomB, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          dtc::mma_ss_if(lead, acc + DP, dm + kk * kRows16, dc + kk * kRows16, id_u, kk > 0 ? 1u : 0u);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        dtc::mma_ss_if(lead, acc + DP, dl + kk * kRows16, dc + kk * kRows16, id_u, DP > 64 || kk > 0 ? 1u : 0u);
+      dtc::commit_if(lead, bar(ms->done[i & 1]));
+      dtc::commit_if(lead, bar(ms->empty[s]));
+    }
+    dtc::commit_if(lead, bar(ms->drain));
+    __syncwarp();
+    mbar_wait(bar(ms->drain), 0, nullptr, kWaitLimitCycles / 8);
+    __syncwarp();
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ w b (thread = every 32nd row of each 64 columns)
+    const int t = tid - 128, r0 = t >> 3;
+    const uint64_t m1 = dtc::pair(-1.f, -1.f);
+    double cf = 1.0;  // decay over the segment's tokens beyond the chunk
+    const double full = dcy::decay_pow(p.log_decay[h], kTok);
+    for (int i = 0; i < N; ++i) {
+      const int s = i % C::NS, n = tokens(i);
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 32 * k;
+        w[k] = r < n ? ms->pw[rev ? r + 1 : n - 1 - r] * (float)cf : 0.f;
+      }
+      cf *= n == kTok ? full : dcy::decay_pow(p.log_decay[h], n);
+      if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) break;
+      if (i >= C::NT && !mbar_wait(bar(ms->done[(i - C::NT) & 1]), ((i - C::NT) >> 1) & 1, abort_flag)) break;
+      uint8_t* hi = gb + s * C::kStageB + 16 * t;
+      uint8_t* lo = gb + C::kTerms + (i % C::NT) * 2 * C::kOpB + 16 * t;
+      uint8_t* mid = lo + C::kOpB;
+#pragma unroll 1
+      for (int x = 0; x < C::NB; ++x) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(hi + x * kAtomB + k * 4096);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t ww = dtc::pair(w[k], w[k]);
+          uint32_t ph[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, pm[4], pl[4];
+          const bool past = r0 + 32 * k >= n;  // rows behind the end may hold anything
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t u = dtc::mul2(dtc::pair(ph[q] << 16, ph[q] & 0xffff0000u), ww);
+            ph[q] = dtc::pack2(u);
+            const uint64_t u1 = dtc::fma2(dtc::pair(ph[q] << 16, ph[q] & 0xffff0000u), m1, u);
+            pm[q] = dtc::pack2(u1);
+            pl[q] = dtc::pack2(dtc::fma2(dtc::pair(pm[q] << 16, pm[q] & 0xffff0000u), m1, u1));
+            if (past) ph[q] = pm[q] = pl[q] = 0u;
+          }
+          *reinterpret_cast<uint4*>(hi + x * kAtomB + k * 4096) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+          *reinterpret_cast<uint4*>(mid + x * kAtomB + k * 4096) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
+          *reinterpret_cast<uint4*>(lo + x * kAtomB + k * 4096) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+        }
+      }
+      if (n < kTok) {  // rows of c behind the end take part in products with zero: they must be finite
+        uint8_t* cc = gb + s * C::kStageB + C::kOpB;
+        for (int e = t; e < C::kOpB / 16; e += 256)
+          if (((e >> 3) & (kTok - 1)) >= n) *reinterpret_cast<uint4*>(cc + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ms->t_full[i & 1]));
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ running sums (thread = row of X, 64 columns)
+    const int q4 = warp & 3, row = q4 * 32 + lane, col0 = DP > 64 ? 64 * ((warp - 12) >> 2) : 0;
+    const uint32_t la = uint32_t(q4 * 32) << 16;
+    const bool second = DP > 64 || q4 < 2;  // d <= 64: rows 64.. of the second accumulator are unused
+    float x[64];
+#pragma unroll
+    for (int e = 0; e < 64; ++e) x[e] = 0.f;
+    bool ok = true;
+    for (int i = 0; i < N; ++i) {
+      if (!(ok = mbar_wait(bar(ms->done[i & 1]), (i >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + la + (i & 1) * C::kAcc + col0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t v[16];
+        if (second) {  // the small terms first
+          tmem_ld16(acc + DP + 16 * y, v);
+          tmem_wait_ld();
+          uint32_t u[16];
+          tmem_ld16(acc + 16 * y, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[16 * y + e] += __uint_as_float(u[e]) + __uint_as_float(v[e]);
+        } else {
+          tmem_ld16(acc + 16 * y, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[16 * y + e] += __uint_as_float(v[e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ms->d_free[i & 1]));
+    }
+    if (DP == 64) {  // rows 64.. hold the mid terms' sums: through shared memory to rows 0 .. 63
+      uint32_t ph = 0;
+      float* scr = reinterpret_cast<float*>(gb + C::kTerms);  // free: the last product is done
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && row >= 64) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) scr[e * 64 + row - 64] = x[e];
+      }
+      ok = group_sync(bar(ms->sync), ph, abort_flag) && ok;
+      if (ok && row < 64) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) x[e] += scr[e * 64 + row];
+      }
+    }
+    if (ok && row < d && row < DP && (DP > 64 || row < 64)) {
+      const long long dd = (long long)d * d;
+      float* out = p.ws ? p.ws + (((long long)jid * p.B * p.H + bh) * p.nseg + seg) * dd : job.out + bh * dd;
+      const float* in = !p.ws && job.in ? job.in + bh * dd : nullptr;
+      const double f = in ? dcy::decay_pow(p.log_decay[h], len) : 0.0;
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        if (col0 + e >= d) continue;
+        const long long at = (long long)row * d + col0 + e;
+        float4 y = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        if (in) {
+          const float4 z = *reinterpret_cast<const float4*>(in + at);
+          y = make_float4((float)(f * z.x + y.x), (float)(f * z.y + y.y), (float)(f * z.z + y.z),
+                          (float)(f * z.w + y.w));
+        }
+        *reinterpret_cast<float4*>(out + at) = y;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(ms->tmem_base, C::kCols);
+  }
+  pdl_wait();  // where this kernel was started beside the walk: it ends after it
+}
+
+}  // namespace dst
+}  // namespace favor

@@ -13,22 +13,22 @@
 //   state     X <- lambda^n X + (w B)^T C                 d x d x 128
 // Every exponent is >= 0: lambda = 0 and strong decays need no division and lose nothing.
 //
-// Precision. The state stays in fp32 in TMEM; each chunk it is read once, scaled by lambda^n, written
-// back, and its bf16 image goes to shared memory for A X. The update accumulates onto it. Rounding
-// w B to bf16 would cost the fp32 state 2^-9 of every product, so w B goes in as two bf16 terms, hi =
-// bf16(w b) and lo = bf16(w b - hi): 2^-18 per product. hi overwrites B in place once the scores have
-// read it. d <= 64 stacks hi and lo as the 128 rows of one operand (rows 64.. of the state collect the
-// lo products and are added when it is read out; its bf16 image for A X, rounded to 2^-8 itself, takes
-// the hi rows alone: 2^-8 once more of each product); d <= 128 accumulates hi, then lo.
+// Precision. The walk's state serves its bf16 rows; the states a caller gets back are summed to fp32
+// accuracy by kernel_decay_state.cuh. It stays in fp32 in TMEM; each chunk it is read once, scaled by
+// lambda^n, written back, and its bf16 image goes to shared memory for A X. The update accumulates onto
+// it. Rounding w B to bf16 would put a second rounding of 2^-8 on every product that reaches a later
+// chunk, beside the image's, so w B goes in as two bf16 terms, hi = bf16(w b) and lo = bf16(w b - hi). hi
+// overwrites B in place once the scores have read it. d <= 64 stacks hi and lo as the 128 rows of one
+// operand: rows 64.. of the state and of its image are the lo products' sums, and A X reads A twice.
+// d <= 128 accumulates hi, then lo.
 //
-// The state update is the only dependence between chunks: update -> state read and rescaled -> next
-// update, about 1000 cycles against the 2700 in which an SM's share of HBM delivers a d = 64 chunk, so a
-// walk is bound by memory as long as the loads run ahead (2 or 3 chunks) and every other step
-// overlaps. Long sequences of few heads are cut into segments: kernel OUT = false computes each
-// segment's own state from b and c alone, k_chunk_scan carries them, and kernel OUT = true walks all
-// segments at once.
+// What bounds it. An SM's share of HBM delivers a d = 64 chunk in about 2700 cycles and a d = 128 one in
+// 5400; a chunk takes about 2950 and 5550. Shared memory is the busiest unit beside it (the MMAs' operands,
+// the loads, w B in place, the image: about 2300 of its 128-byte cycles a d = 64 chunk). Long sequences of
+// few heads are cut into segments: the state kernel sums each segment's own state from b and c alone,
+// k_chunk_scan carries them, and this kernel walks all segments at once.
 //
-// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-11 w B and state; with OUT 12-19 scores, 20-27
+// Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-11 w B and state; 12-19 scores; 20-27
 // rows out. Thread = row of its 128 (token or state row).
 //
 // Non-finite values. The mask removes a product by selecting zero into P, but zero times an infinity
@@ -53,7 +53,6 @@ constexpr int kAtomB = kTok * 128;  // 128 rows of 64 bf16 columns, 128-byte swi
 struct Job {
   int a, b, c;  // operands (indices into Params::m)
   int state, trans, reverse;
-  int final;    // 1: writes its state's `out` (one segment only)
   View va, vb, vc, y;  // rows in global memory: a, b, c for elements summed again
 };
 
@@ -62,33 +61,32 @@ struct Params {
   int bm[4], hm[4];  // 0 where an operand repeats over batch entries or heads
   Job j[3];
   const float* in[2];  // carried-in states, used where `ws` is null
-  float* out[2];
-  float* ws;           // [states][BH][nseg][d * d]: OUT = false writes it, OUT = true reads it
+  const float* ws;     // [states][BH][nseg][d * d], the states carried into each segment
   const float* log_decay;
   const int* lengths;
   int njobs, B, H, L, d, nseg, cps;  // chunks per segment
 };
 
-template <int DP, bool OUT>
+template <int DP>
 struct Cfg {
   static constexpr int NB = DP / 64;
   static constexpr int kOpB = NB * kAtomB;
-  static constexpr int kStageB = (OUT ? 3 : 2) * kOpB;  // b, c, a
-  static constexpr int NS = DP == 64 ? (OUT ? 3 : 4) : 2;
+  static constexpr int kStageB = 3 * kOpB;  // b, c, a
+  static constexpr int NS = DP == 64 ? 3 : 2;
   static constexpr int NLO = DP == 64 ? 2 : 1;
   static constexpr int kLo = NS * kStageB;
   // d > 64: the image of X and the lo operand share one buffer (the image is read before lo is
   // written), and rows out are staged over the chunk's own A, which every product has read by then.
   static constexpr int NX = DP == 64 ? 2 : 1;
   static constexpr int kX = DP == 64 ? kLo + NLO * kOpB : kLo;
-  static constexpr int kY = kX + (OUT || DP > 64 ? NX * kOpB : 0);
-  static constexpr int kMisc = kY + (OUT && DP == 64 ? kOpB : 0);
+  static constexpr int kY = kX + NX * kOpB;
+  static constexpr int kMisc = kY + (DP == 64 ? kOpB : 0);
   static constexpr int kSmem = kMisc + 2048 + 1024;
-  static constexpr int kThreads = OUT ? 896 : 384;
-  static constexpr int kBT = OUT && DP == 64 ? 128 : 256;  // threads that weight B
-  static constexpr int SB = OUT && DP == 64 ? 2 : 1;  // score buffers
+  static constexpr int kThreads = 896;
+  static constexpr int kBT = DP == 64 ? 128 : 256;  // threads that weight B
+  static constexpr int SB = DP == 64 ? 2 : 1;  // score buffers
   static constexpr uint32_t kTO1 = DP, kTO2 = 2 * DP, kTS = DP == 64 ? 192 : 384;
-  static constexpr uint32_t kCols = OUT ? 512 : DP;
+  static constexpr uint32_t kCols = 512;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -99,7 +97,7 @@ struct Misc {
   float pwz[64];               // 31 zeros, then lambda^0 .. lambda^31
   uint64_t full[4], empty[4];
   uint64_t s_full[2], p_full[2];
-  uint64_t x_full, img_full[2], qx_done, pc_done[2], bh_full[2], u_done[2], o_full, o_free, st_sync, drain;
+  uint64_t x_full, img_full[2], qx_done, pc_done[2], bh_full[2], u_done[2], o_full, o_free, drain;
 };
 static_assert(sizeof(Misc) <= 2048, "misc block");
 
@@ -186,22 +184,6 @@ __device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
   x[4] = bf_lo(u.z), x[5] = bf_hi(u.z), x[6] = bf_lo(u.w), x[7] = bf_hi(u.w);
 }
 
-// d <= 64: rows 64.. of the state hold the lo products' sums; one 32-column block of them added to rows
-// 0 .. 63 through `scr` (8 KB), by the 128 threads of the state's rows. False after a timeout.
-__device__ __forceinline__ bool fold_lo(uint32_t (&v)[32], float* scr, int row, Misc* ms, uint32_t& ph) {
-  if (!__all_sync(0xffffffffu, group_sync(smem_u32(&ms->st_sync), ph, &ms->abort_flag))) return false;
-  if (row >= 64) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) scr[e * 64 + row - 64] = __uint_as_float(v[e]);
-  }
-  if (!__all_sync(0xffffffffu, group_sync(smem_u32(&ms->st_sync), ph, &ms->abort_flag))) return false;
-  if (row < 64) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + scr[e * 64 + row]);
-  }
-  return true;
-}
-
 // Columns 32 x .. of one row of X from a [d, d] state, or its transpose; zeros where there is none.
 __device__ __forceinline__ void load_state(uint32_t (&v)[32], const float* in, int x, int row, int d, int trans) {
 #pragma unroll
@@ -221,25 +203,9 @@ __device__ __forceinline__ void load_state(uint32_t (&v)[32], const float* in, i
   }
 }
 
-// Columns 32 x .. of one row of X to a [d, d] state, or its transpose.
-__device__ __forceinline__ void store_state(float* out, const uint32_t (&v)[32], int x, int row, int d, int dp,
-                                            int trans) {
-  if (row >= d || row >= dp) return;
-  if (trans) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (32 * x + e < d) out[(32 * x + e) * d + row] = __uint_as_float(v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      if (32 * x + e < d)
-        *reinterpret_cast<uint4*>(out + row * d + 32 * x + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-  }
-}
-
-template <int DP, bool OUT>
-__global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const __grid_constant__ Params p) {
-  using C = Cfg<DP, OUT>;
+template <int DP>
+__global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __grid_constant__ Params p) {
+  using C = Cfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -259,29 +225,22 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
   const int nch = (int)(((long long)len + kTok - 1) / kTok);
   const int c0 = seg * p.cps, c1 = min(nch, c0 + p.cps);
   const int N = c1 - c0;  // chunks to walk
-  const float* x_in = p.ws && OUT ? p.ws + (((long long)job.state * p.B * p.H + bh) * p.nseg + seg) * d * d
-                      : OUT && p.in[job.state] ? p.in[job.state] + (long long)bh * d * d
-                                               : nullptr;
-  float* x_out = !OUT ? p.ws + (((long long)job.state * p.B * p.H + bh) * p.nseg + seg) * d * d
-                 : job.final && p.out[job.state] ? p.out[job.state] + (long long)bh * d * d
-                                                 : nullptr;
-  // a segment behind the sequence's end; an empty sequence still hands its state on
-  if (N <= 0 && !(OUT && x_out)) {
+  const float* x_in = p.ws ? p.ws + (((long long)job.state * p.B * p.H + bh) * p.nseg + seg) * d * d
+                      : p.in[job.state] ? p.in[job.state] + (long long)bh * d * d
+                                        : nullptr;
+  if (N <= 0) {  // a segment behind the sequence's end
     pdl_launch_dependents();
-    if (OUT) pdl_wait();
+    pdl_wait();
     return;
   }
-
-  // OUT walks with the job's direction; the states alone are summed against it, so that each chunk's
-  // factor (the decay over the segment's tokens beyond it) grows from 1 by one product a chunk
-  auto chunk = [&](int i) { return (rev != 0) == OUT ? c1 - 1 - i : c0 + i; };
+  auto chunk = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
   auto tokens = [&](int i) { return min(kTok, len - chunk(i) * kTok); };
   const int op[3] = {job.b, job.c, job.a};
   auto load = [&](int i) {  // one lane: chunk i into its stage
     const int s = i % C::NS, row = chunk(i) * kTok;
     mbar_arrive_expect_tx(bar(ms->full[s]), C::kStageB);
 #pragma unroll
-    for (int o = 0; o < (OUT ? 3 : 2); ++o)
+    for (int o = 0; o < 3; ++o)
 #pragma unroll
       for (int x = 0; x < C::NB; ++x)
         tma_load_4d(base + s * C::kStageB + o * C::kOpB + x * kAtomB, &p.m[op[o]], bar(ms->full[s]), 64 * x, row,
@@ -291,7 +250,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     ms->abort_flag = 0;
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(bar(ms->full[s]), 1);
-      mbar_init(bar(ms->empty[s]), OUT && DP > 64 ? 9 : 1);  // the last MMA's commit; rows staged over a
+      mbar_init(bar(ms->empty[s]), DP > 64 ? 9 : 1);  // the last MMA's commit; rows staged over a
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(ms->s_full[s]), 1);
@@ -305,7 +264,6 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     mbar_init(bar(ms->qx_done), 1);
     mbar_init(bar(ms->o_full), 1);
     mbar_init(bar(ms->o_free), 8);
-    mbar_init(bar(ms->st_sync), 128);
     mbar_init(bar(ms->drain), 1);
     fence_mbar_init();
     for (int i = 0; i < min(N, C::NS); ++i) load(i);  // in flight while the block sets up
@@ -327,8 +285,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  // all 512 columns start at column 0; fewer, where the allocator put them
-  const uint32_t tmem = C::kCols == 512 ? 0u : __shfl_sync(0xffffffffu, ms->tmem_base, 0);
+  constexpr uint32_t tmem = 0;  // all 512 columns are this block's
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -372,7 +329,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     auto update = [&](int i, bool last) {  // last: of the chunk's products, as below
       const int s = i % C::NS;
       mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
-      if (OUT) mbar_wait(bar(ms->x_full), i & 1, abort_flag);
+      mbar_wait(bar(ms->x_full), i & 1, abort_flag);
       mbar_wait(bar(ms->bh_full[i & 1]), (i >> 1) & 1, abort_flag);
       tc_fence_after();
       const uint32_t st = base + s * C::kStageB, lo = base + C::kLo + (i % C::NLO) * C::kOpB;
@@ -380,7 +337,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       const uint64_t dw = sdesc_sw128(st, DP == 64 ? lo - st : kAtomB, 1024);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        mma_ss_if(lead, tmem, dw + kk * kRows16, dc + kk * kRows16, id_u, OUT || i > 0 || kk > 0 ? 1u : 0u);
+        mma_ss_if(lead, tmem, dw + kk * kRows16, dc + kk * kRows16, id_u, 1u);
       if (DP > 64) {
         const uint64_t dl = sdesc_sw128(lo, kAtomB, 1024);
 #pragma unroll
@@ -397,8 +354,8 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       const uint64_t da = sdesc_sw128(base + (i % C::NS) * C::kStageB + 2 * C::kOpB, 16, 1024);
       const uint64_t dx = sdesc_sw128(base + C::kX + (i % C::NX) * C::kOpB, kAtomB, 1024);
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk)
-        mma_ss_if(lead, tmem + C::kTO1, da + kmaj(kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < 8; ++kk)  // 128 rows of X: hi and lo (d <= 64), or d
+        mma_ss_if(lead, tmem + C::kTO1, da + kmaj(DP == 64 ? kk & 3 : kk), dx + kk * kRows16, id_x, kk > 0 ? 1u : 0u);
       if (DP > 64) commit_if(lead, bar(ms->qx_done));
     };
     // P C
@@ -418,11 +375,9 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     // With one score buffer (d > 64) that is this chunk's; and the update follows A X, whose image its lo
     // operand overwrites, and P C, which lets the rows out start, but where the update's operand pass
     // zeroes c's tail.
-    if (OUT && N > 0) scores(0);
+    scores(0);
     for (int i = 0; i < N; ++i) {
-      if (!OUT) {
-        update(i, true);
-      } else if (C::SB == 2) {
+      if (C::SB == 2) {
         if (i + 1 < N) scores(i + 1);
         update(i, false);
         carried(i);
@@ -448,31 +403,28 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
     // take half the state's columns, then half of w B.
     constexpr int T = C::kBT;
     constexpr int NR = kTok / (T / 8);
-    const bool does_b = !OUT || DP > 64 || warp < 8, does_x = OUT && (DP > 64 || warp >= 8);
+    const bool does_b = DP > 64 || warp < 8, does_x = DP > 64 || warp >= 8;
     const int t = tid - 128, r0 = t >> 3;
     const int q4 = warp & 3, row = q4 * 32 + lane, half = DP > 64 ? (warp - 4) >> 2 : 0;
     const uint32_t la = uint32_t(q4 * 32) << 16;
     const uint64_t m1 = pair(-1.f, -1.f);
-    float* scr = reinterpret_cast<float*>(gb + C::kLo);  // free once the last update is done
-    float w[NR], cf = 1.f;
+    float w[NR];
     int nw = 0;  // tokens the weights are for
-    uint32_t ph = 0;
     auto scale_b = [&](int i) -> bool {
       const int s = i % C::NS, n = tokens(i);
-      if (n != nw || !OUT) {
+      if (n != nw) {
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
           const int r = r0 + k * (T / 8);
-          w[k] = r < n ? ms->pw[rev ? r + 1 : n - 1 - r] * cf : 0.f;
+          w[k] = r < n ? ms->pw[rev ? r + 1 : n - 1 - r] : 0.f;
         }
         nw = n;
-        if (!OUT) cf *= ms->pw[n];
       }
       if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) return false;
       // the lo buffer's last reader is update i - NLO
       if (i >= C::NLO && !mbar_wait(bar(ms->u_done[(i - C::NLO) & 1]), ((i - C::NLO) >> 1) & 1, abort_flag)) return false;
-      if (OUT && !mbar_wait(bar(ms->s_full[i % C::SB]), (i / C::SB) & 1, abort_flag)) return false;  // B has been read
-      if (OUT && DP > 64 && !mbar_wait(bar(ms->qx_done), i & 1, abort_flag)) return false;           // so has X's image
+      if (!mbar_wait(bar(ms->s_full[i % C::SB]), (i / C::SB) & 1, abort_flag)) return false;  // B has been read
+      if (DP > 64 && !mbar_wait(bar(ms->qx_done), i & 1, abort_flag)) return false;           // so has X's image
       uint8_t* hi = gb + s * C::kStageB + 16 * t;
       uint8_t* lo = gb + C::kLo + (i % C::NLO) * C::kOpB + 16 * t;
 #pragma unroll 1
@@ -524,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
         } else {
           load_state(v, x_in, x, row, d, job.trans);
         }
-        if (DP > 64 || row < 64) {
+        {
           uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -544,21 +496,6 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms->img_full[i & 1]));
     };
-    // X behind the last chunk, to memory
-    auto write_out = [&]() {
-#pragma unroll 1
-      for (int x = 2 * half; x < 2 * half + 2; ++x) {
-        uint32_t v[32];
-        if (N > 0) {
-          tmem_ld32(tmem + la + 32 * x, v);
-          tmem_wait_ld();
-          if (DP == 64 && !fold_lo(v, scr, row, ms, ph)) return;
-        } else {
-          load_state(v, x_in, x, row, d, job.trans);
-        }
-        store_state(x_out, v, x, row, d, DP, job.trans);
-      }
-    };
     auto updated = [&](int i) -> bool {
       const bool ok = mbar_wait(bar(ms->u_done[i & 1]), (i >> 1) & 1, abort_flag);
       tc_fence_after();
@@ -573,8 +510,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       }
       if (does_b) ok = scale_b(i);
     }
-    if (ok && x_out && (does_x || (!OUT && (DP > 64 || warp < 8))) && (N <= 0 || updated(N - 1))) write_out();
-  } else if (OUT && warp >= 12 && warp < 20) {
+  } else if (warp >= 12 && warp < 20) {
     // ------------------------------------------------------------ scores -> P (thread = row, half the columns)
     const int q4 = warp & 3, row = q4 * 32 + lane, half = (warp - 12) >> 2;
     const uint32_t la = uint32_t(q4 * 32) << 16;
@@ -652,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms->p_full[sb]));
     }
-  } else if (OUT && warp >= 20) {
+  } else if (warp >= 20) {
     // ------------------------------------------------------------ rows out (thread = row, half the columns)
     const int q4 = warp & 3, row = q4 * 32 + lane, half = (warp - 20) >> 2;
     const uint32_t la = uint32_t(q4 * 32) << 16;
@@ -762,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<DP, OUT>::kThreads, 1) k_decay_walk(const 
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kCols);
+    tmem_dealloc(ms->tmem_base, C::kCols);
   }
 }
 
