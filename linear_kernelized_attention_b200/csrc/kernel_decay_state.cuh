@@ -16,7 +16,9 @@
 // Chunks are taken against the state's direction, so that a chunk's factor, the decay over the tokens
 // beyond it, grows from 1 by one product (in double) a chunk, and nothing is ever rescaled.
 //
-// Reading b and c bounds it: 32 KB a chunk and head at d = 64.
+// Reading b and c bounds it at best: 32 KB a chunk and head at d = 64. Terms are made in units of 8192
+// elements (128 tokens, or 64 at d > 64) with two buffers, so that one unit's products run beside the next
+// one's arithmetic.
 //
 // Warps: 0 TMA; 1 TMEM allocation and MMAs; 4-11 the three terms of w b (hi in place, mid and lo beside
 // it); 12-15 (d <= 64) or 12-19 the running sums, thread = row of X (b's column).
@@ -53,13 +55,15 @@ struct Cfg {
   static constexpr int kOpB = NB * kAtomB;
   static constexpr int kStageB = 2 * kOpB;  // b, c
   static constexpr int NS = DP == 64 ? 4 : 2;
-  static constexpr int NT = DP == 64 ? 2 : 1;       // buffers of (lo, mid)
+  static constexpr int UPC = NB;                    // units of terms a chunk: 128 tokens of 64 columns, or 64 of 128
+  static constexpr int kUnitB = kOpB / UPC, kUnitAtomB = kAtomB / UPC;
+  static constexpr int NT = 2;                      // buffers of a unit's (lo, mid)
   static constexpr int kTerms = NS * kStageB;
-  static constexpr int kMisc = kTerms + NT * 2 * kOpB;
+  static constexpr int kMisc = kTerms + NT * 2 * kUnitB;
   static constexpr int kSmem = kMisc + 2048 + 1024;
   static constexpr int kThreads = DP == 64 ? 512 : 640;
   static constexpr uint32_t kAcc = 2 * DP;          // columns of one chunk's accumulators: hi (and mid), the rest
-  static constexpr uint32_t kCols = 2 * kAcc;
+  static constexpr uint32_t kCols = 512;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -67,7 +71,7 @@ struct Misc {
   int abort_flag;
   uint32_t tmem_base;
   float pw[132];  // lambda^0 .. lambda^128
-  uint64_t full[4], empty[4], t_full[2], done[2], d_free[2], sync, drain;
+  uint64_t full[4], empty[4], t_full[2], t_free[2], done[2], d_free[2], sync, drain;
 };
 
 template <int DP>
@@ -116,8 +120,11 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
       mbar_init(bar(ms->full[s]), 1);
       mbar_init(bar(ms->empty[s]), 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::NT; ++s) {
       mbar_init(bar(ms->t_full[s]), 8);
+      mbar_init(bar(ms->t_free[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(bar(ms->done[s]), 1);
       mbar_init(bar(ms->d_free[s]), DP / 16);
     }
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, ms->tmem_base, 0);
+  constexpr uint32_t tmem = 0;  // all 512 columns are this block's
 
   if (warp == 0) {
     const bool leader = elect_one();
@@ -158,26 +165,31 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
     for (int i = 0; i < N; ++i) {
       const int s = i % C::NS;
       mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag);
-      mbar_wait(bar(ms->t_full[i & 1]), (i >> 1) & 1, abort_flag);
       if (i >= 2) mbar_wait(bar(ms->d_free[i & 1]), ((i >> 1) - 1) & 1, abort_flag);
-      tc_fence_after();
-      const uint32_t hi = base + s * C::kStageB, lo = base + C::kTerms + (i % C::NT) * 2 * C::kOpB, mid = lo + C::kOpB;
       const uint32_t acc = tmem + (i & 1) * C::kAcc;
-      const uint64_t dc = sdesc_sw128(hi + C::kOpB, kAtomB, 1024);
-      const uint64_t dh = sdesc_sw128(hi, DP == 64 ? mid - hi : kAtomB, 1024);
-      const uint64_t dl = sdesc_sw128(lo, kAtomB, 1024);  // d <= 64: mid is its second half
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        dtc::mma_ss_if(lead, acc, dh + kk * kRows16, dc + kk * kRows16, id_u, kk > 0 ? 1u : 0u);
-      if (DP > 64) {
-        const uint64_t dm = sdesc_sw128(mid, kAtomB, 1024);
+      for (int f = 0; f < C::UPC; ++f) {
+        const int u = C::UPC * i + f, t = u % C::NT;
+        mbar_wait(bar(ms->t_full[t]), (u / C::NT) & 1, abort_flag);
+        tc_fence_after();
+        const uint32_t hi = base + s * C::kStageB + f * C::kUnitAtomB, lo = base + C::kTerms + t * 2 * C::kUnitB, mid = lo + C::kUnitB;
+        const uint64_t dc = sdesc_sw128(hi + C::kOpB, kAtomB, 1024);
+        const uint64_t dh = sdesc_sw128(hi, DP == 64 ? mid - hi : kAtomB, 1024);
+        const uint64_t dl = sdesc_sw128(lo, C::kUnitAtomB, 1024);  // d <= 64: mid is its second half
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          dtc::mma_ss_if(lead, acc + DP, dm + kk * kRows16, dc + kk * kRows16, id_u, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 8 / C::UPC; ++kk)
+          dtc::mma_ss_if(lead, acc, dh + kk * kRows16, dc + kk * kRows16, id_u, f > 0 || kk > 0 ? 1u : 0u);
+        if (DP > 64) {
+          const uint64_t dm = sdesc_sw128(mid, C::kUnitAtomB, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8 / C::UPC; ++kk)
+            dtc::mma_ss_if(lead, acc + DP, dm + kk * kRows16, dc + kk * kRows16, id_u, f > 0 || kk > 0 ? 1u : 0u);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 8 / C::UPC; ++kk)
+          dtc::mma_ss_if(lead, acc + DP, dl + kk * kRows16, dc + kk * kRows16, id_u, DP > 64 || f > 0 || kk > 0 ? 1u : 0u);
+        dtc::commit_if(lead, bar(ms->t_free[t]));
       }
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        dtc::mma_ss_if(lead, acc + DP, dl + kk * kRows16, dc + kk * kRows16, id_u, DP > 64 || kk > 0 ? 1u : 0u);
       dtc::commit_if(lead, bar(ms->done[i & 1]));
       dtc::commit_if(lead, bar(ms->empty[s]));
     }
@@ -186,57 +198,57 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
     mbar_wait(bar(ms->drain), 0, nullptr, kWaitLimitCycles / 8);
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------------------ w b (thread = every 32nd row of each 64 columns)
+    // ------------------------------------------------------------ w b, a unit at a time
+    constexpr int UR = kTok / C::UPC, NR = UR / 32;  // rows of a unit, and of a thread in each 64 columns
     const int t = tid - 128, r0 = t >> 3;
     const uint64_t m1 = dtc::pair(-1.f, -1.f);
     double cf = 1.0;  // decay over the segment's tokens beyond the chunk
     const double full = dcy::decay_pow(p.log_decay[h], kTok);
-    for (int i = 0; i < N; ++i) {
-      const int s = i % C::NS, n = tokens(i);
-      float w[4];
+    for (int u = 0; u < C::UPC * N; ++u) {
+      const int i = u / C::UPC, f = u % C::UPC, s = i % C::NS, n = tokens(i), tb = u % C::NT;
+      float w[NR];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = r0 + 32 * k;
+      for (int k = 0; k < NR; ++k) {
+        const int r = UR * f + r0 + 32 * k;
         w[k] = r < n ? ms->pw[rev ? r + 1 : n - 1 - r] * (float)cf : 0.f;
       }
-      cf *= n == kTok ? full : dcy::decay_pow(p.log_decay[h], n);
+      if (f == C::UPC - 1) cf *= n == kTok ? full : dcy::decay_pow(p.log_decay[h], n);
       if (!mbar_wait(bar(ms->full[s]), (i / C::NS) & 1, abort_flag)) break;
-      if (i >= C::NT && !mbar_wait(bar(ms->done[(i - C::NT) & 1]), ((i - C::NT) >> 1) & 1, abort_flag)) break;
-      uint8_t* hi = gb + s * C::kStageB + 16 * t;
-      uint8_t* lo = gb + C::kTerms + (i % C::NT) * 2 * C::kOpB + 16 * t;
-      uint8_t* mid = lo + C::kOpB;
-#pragma unroll 1
-      for (int x = 0; x < C::NB; ++x) {
-        uint4 v[4];
+      if (u >= C::NT && !mbar_wait(bar(ms->t_free[tb]), ((u / C::NT) - 1) & 1, abort_flag)) break;
+      uint8_t* hi = gb + s * C::kStageB + C::kUnitAtomB * f + 16 * t;
+      uint8_t* lo = gb + C::kTerms + tb * 2 * C::kUnitB + 16 * t;
+      uint8_t* mid = lo + C::kUnitB;
+      uint4 v[4];  // NB atoms x NR rows
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(hi + x * kAtomB + k * 4096);
+      for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(hi + (k / NR) * kAtomB + (k % NR) * 4096);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t ww = dtc::pair(w[k], w[k]);
-          uint32_t ph[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, pm[4], pl[4];
-          const bool past = r0 + 32 * k >= n;  // rows behind the end may hold anything
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t ww = dtc::pair(w[k % NR], w[k % NR]);
+        uint32_t ph[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, pm[4], pl[4];
+        const bool past = UR * f + r0 + 32 * (k % NR) >= n;  // rows behind the end may hold anything
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint64_t u = dtc::mul2(dtc::pair(ph[q] << 16, ph[q] & 0xffff0000u), ww);
-            ph[q] = dtc::pack2(u);
-            const uint64_t u1 = dtc::fma2(dtc::pair(ph[q] << 16, ph[q] & 0xffff0000u), m1, u);
-            pm[q] = dtc::pack2(u1);
-            pl[q] = dtc::pack2(dtc::fma2(dtc::pair(pm[q] << 16, pm[q] & 0xffff0000u), m1, u1));
-            if (past) ph[q] = pm[q] = pl[q] = 0u;
-          }
-          *reinterpret_cast<uint4*>(hi + x * kAtomB + k * 4096) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          *reinterpret_cast<uint4*>(mid + x * kAtomB + k * 4096) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
-          *reinterpret_cast<uint4*>(lo + x * kAtomB + k * 4096) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t y = dtc::mul2(dtc::pair(ph[q] << 16, ph[q] & 0xffff0000u), ww);
+          ph[q] = dtc::pack2(y);
+          const uint64_t y1 = dtc::fma2(dtc::pair(ph[q] << 16, ph[q] & 0xffff0000u), m1, y);
+          pm[q] = dtc::pack2(y1);
+          pl[q] = dtc::pack2(dtc::fma2(dtc::pair(pm[q] << 16, pm[q] & 0xffff0000u), m1, y1));
+          if (past) ph[q] = pm[q] = pl[q] = 0u;
         }
+        *reinterpret_cast<uint4*>(hi + (k / NR) * kAtomB + (k % NR) * 4096) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+        *reinterpret_cast<uint4*>(mid + (k / NR) * C::kUnitAtomB + (k % NR) * 4096) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
+        *reinterpret_cast<uint4*>(lo + (k / NR) * C::kUnitAtomB + (k % NR) * 4096) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
       }
-      if (n < kTok) {  // rows of c behind the end take part in products with zero: they must be finite
+      if (n < UR * f + UR) {  // rows of c behind the end take part in products with zero: they must be finite
         uint8_t* cc = gb + s * C::kStageB + C::kOpB;
-        for (int e = t; e < C::kOpB / 16; e += 256)
-          if (((e >> 3) & (kTok - 1)) >= n) *reinterpret_cast<uint4*>(cc + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = t; e < C::kOpB / 16; e += 256) {
+          const int r = (e >> 3) & (kTok - 1);
+          if (r >= n && r / UR == f) *reinterpret_cast<uint4*>(cc + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(ms->t_full[i & 1]));
+      if (lane == 0) mbar_arrive(bar(ms->t_full[tb]));
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ running sums (thread = row of X, 64 columns)
@@ -252,22 +264,17 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
       tc_fence_after();
       const uint32_t acc = tmem + la + (i & 1) * C::kAcc + col0;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        uint32_t v[16];
-        if (second) {  // the small terms first
-          tmem_ld16(acc + DP + 16 * y, v);
-          tmem_wait_ld();
-          uint32_t u[16];
-          tmem_ld16(acc + 16 * y, u);
-          tmem_wait_ld();
+      for (int y = 0; y < 64; y += 8) {
+        uint32_t v[8], u[8];
+        if (second) tmem_ld8(acc + DP + y, v);
+        tmem_ld8(acc + y, u);
+        tmem_wait_ld();
+        if (second) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[16 * y + e] += __uint_as_float(u[e]) + __uint_as_float(v[e]);
-        } else {
-          tmem_ld16(acc + 16 * y, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[16 * y + e] += __uint_as_float(v[e]);
+          for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(v[e]));
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[y + e] += __uint_as_float(u[e]);
       }
       tc_fence_before();
       __syncwarp();

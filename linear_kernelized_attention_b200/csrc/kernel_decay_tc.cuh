@@ -470,12 +470,8 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
 #pragma unroll 1
       for (int x = 2 * half; x < 2 * half + 2; ++x) {
         uint32_t v[32];
-        if (i > 0) {
-          tmem_ld32(tmem + la + 32 * x, v);
-          tmem_wait_ld();
-        } else {
-          load_state(v, x_in, x, row, d, job.trans);
-        }
+        tmem_ld32(tmem + la + 32 * x, v);
+        tmem_wait_ld();
         {
           uint8_t* img = gb + C::kX + (i % C::NX) * C::kOpB + (x >> 1) * kAtomB + row * 128;
 #pragma unroll
@@ -501,7 +497,16 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
       tc_fence_after();
       return __all_sync(0xffffffffu, ok);
     };
-    if (does_x && x_in) pdl_wait();  // the carried states are written by the kernel before
+    if (does_x) {  // X carried in, to TMEM
+      if (x_in) pdl_wait();  // written by the kernel before
+#pragma unroll 1
+      for (int x = 2 * half; x < 2 * half + 2; ++x) {
+        uint32_t v[32];
+        load_state(v, x_in, x, row, d, job.trans);
+        tmem_st32(tmem + la + 32 * x, v);
+      }
+      tmem_wait_st();
+    }
     bool ok = true;
     for (int i = 0; ok && i < N; ++i) {
       if (does_x) {
