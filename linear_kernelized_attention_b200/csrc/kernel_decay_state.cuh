@@ -85,14 +85,17 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
   volatile int* abort_flag = &ms->abort_flag;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // What decides control flow is broadcast from lane 0, so that the compiler knows it to be uniform: loop
+  // counters and MMA descriptors then live in uniform registers (otherwise an MMA takes 100 to 150 cycles to
+  // issue; the products themselves take 32 to 64).
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int jid = blockIdx.x % p.njobs;
   const int seg = (blockIdx.x / p.njobs) % p.nseg;
   const int bh = blockIdx.x / p.njobs / p.nseg;
   const int b = bh / p.H, h = bh % p.H;
   const Job& job = p.j[jid];
   const int rev = job.reverse, d = p.d;
-  const int len = dcy::seq_len(p.lengths, b, p.L);
+  const int len = __shfl_sync(0xffffffffu, dcy::seq_len(p.lengths, b, p.L), 0);
   const int nch = (int)(((long long)len + kTok - 1) / kTok);
   const int c0 = seg * p.cps, c1 = min(nch, c0 + p.cps);
   const int N = max(0, c1 - c0);

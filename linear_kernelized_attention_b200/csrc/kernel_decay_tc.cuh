@@ -214,14 +214,17 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
   volatile int* abort_flag = &ms->abort_flag;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // What decides control flow is broadcast from lane 0, so that the compiler knows it to be uniform: loop
+  // counters and MMA descriptors then live in uniform registers (otherwise an MMA takes 100 to 150 cycles to
+  // issue; the products themselves take 32 to 64).
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int jid = blockIdx.x % p.njobs;
   const int seg = (blockIdx.x / p.njobs) % p.nseg;
   const int bh = blockIdx.x / p.njobs / p.nseg;
   const int b = bh / p.H, h = bh % p.H;
   const Job& job = p.j[jid];
   const int rev = job.reverse, d = p.d;
-  const int len = dcy::seq_len(p.lengths, b, p.L);
+  const int len = __shfl_sync(0xffffffffu, dcy::seq_len(p.lengths, b, p.L), 0);
   const int nch = (int)(((long long)len + kTok - 1) / kTok);
   const int c0 = seg * p.cps, c1 = min(nch, c0 + p.cps);
   const int N = c1 - c0;  // chunks to walk
@@ -376,6 +379,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
     // operand overwrites, and P C, which lets the rows out start, but where the update's operand pass
     // zeroes c's tail.
     scores(0);
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       if (C::SB == 2) {
         if (i + 1 < N) scores(i + 1);
@@ -385,9 +389,13 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
       } else {
         const bool tail = tokens(i) < kTok;
         carried(i);
-        if (tail) update(i, false);
-        values(i, tail);
-        if (!tail) update(i, true);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          if ((k == 0) == tail)
+            update(i, k == 1);
+          else
+            values(i, k == 1);
+        }
         if (i + 1 < N) scores(i + 1);
       }
     }
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
     constexpr int NR = kTok / (T / 8);
     const bool does_b = DP > 64 || warp < 8, does_x = DP > 64 || warp >= 8;
     const int t = tid - 128, r0 = t >> 3;
-    const int q4 = warp & 3, row = q4 * 32 + lane, half = DP > 64 ? (warp - 4) >> 2 : 0;
+    const int q4 = warp & 3, row = q4 * 32 + lane, half = DP > 64 ? t >> 7 : 0;
     const uint32_t la = uint32_t(q4 * 32) << 16;
     const uint64_t m1 = pair(-1.f, -1.f);
     float w[NR];
@@ -508,6 +516,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
       tmem_wait_st();
     }
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; ok && i < N; ++i) {
       if (does_x) {
         if (i > 0 && !(ok = updated(i - 1))) break;
@@ -521,6 +530,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
     const uint32_t la = uint32_t(q4 * 32) << 16;
     const uint64_t l4 = pair(ms->pw[4], ms->pw[4]);
     const float* wz = ms->pwz + 31 + (rev ? -lane : lane);
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       const int sb = i % C::SB, n = tokens(i);
       if (!mbar_wait(bar(ms->s_full[sb]), (i / C::SB) & 1, abort_flag)) break;
@@ -598,6 +608,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
     const int q4 = warp & 3, row = q4 * 32 + lane, half = (warp - 20) >> 2;
     const uint32_t la = uint32_t(q4 * 32) << 16;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(job.y.p) + b * job.y.sb + h * job.y.sh;
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       const int s = i % C::NS, n = tokens(i);
       if (DP == 64) {
