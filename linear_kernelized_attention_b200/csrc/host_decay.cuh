@@ -147,11 +147,11 @@ struct WalkPlan {
 };
 
 // The number of segments with the least estimated time, in microseconds. Measured: a block of the walk takes
-// 3 and 1.6 (d <= 64) or 2.95 a chunk, one of the states alone 3 and 0.75 or 1.4 a chunk, the scan and the
-// gaps of two further launches 6 and a hundredth a segment.
+// 3 and 1.55 (d <= 64) or 2.95 a chunk, one of the states 3 and 1.0 or 2.2 a chunk, the scan and the gaps of
+// two further launches 7 and its traffic at 3 TB/s.
 WalkPlan plan_walk(int BH, int L, int d, int nstates, int njobs) {
   const int nch = (int)(((long long)L + dtc::kTok - 1) / dtc::kTok), sms = sm_count();
-  const double tw = d <= 64 ? 1.6 : 2.95, ts = d <= 64 ? 0.75 : 1.4;
+  const double tw = d <= 64 ? 1.55 : 2.95, ts = d <= 64 ? 1.0 : 2.2;
   auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
   WalkPlan best{};
   double cost = 1e300;
@@ -159,7 +159,7 @@ WalkPlan plan_walk(int BH, int L, int d, int nstates, int njobs) {
     const int cps = (nch + k - 1) / k, nseg = (nch + cps - 1) / cps;
     if (nseg != k) continue;  // as many segments as the chunks per segment need
     double t = waves((long long)BH * njobs * nseg) * (tw * cps + 3.0);
-    if (k > 1) t += waves((long long)BH * nstates * nseg) * (ts * cps + 3.0) + 6.0 + 0.01 * nseg;
+    if (k > 1) t += waves((long long)BH * nstates * nseg) * (ts * cps + 3.0) + 7.0 + 8.0 * BH * nstates * nseg * d * d / 3e6;
     if (t < cost) cost = t, best = WalkPlan{cps, nseg, k > 1};
     if ((long long)BH * nseg > 8ll * sms) break;
   }
