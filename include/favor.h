@@ -289,7 +289,9 @@ int favor_decode_step(const void* q, const void* k, const void* v, const void* o
  *   of no tokens has state_out = state_in.
  * state_in, state_out: device float [B, H, d, d] contiguous (row = k's column, column = v's), 16-byte
  *   aligned, NULL = zeros / not wanted. state_out may be state_in (in place).
- * Supported: 1 <= d <= 128, 1 <= L, dtype_code 0 or 1.
+ * Supported: 1 <= d <= 128, 1 <= L, dtype_code 0 or 1. bf16 operands whose d and strides are multiples of 8
+ * run on the tensor cores: fp32 accumulation, the weighted scores and the carried state rounded to bf16
+ * on their way into `out`; everything else on CUDA cores in fp32. States are returned to fp32 accuracy either way.
  * Infinities and NaN reach what the recurrence takes them to, and nothing before them.
  */
 typedef struct {
@@ -307,7 +309,8 @@ int favor_decay_attention(const void* q, const void* k, const void* v, const flo
  * lengths as the forward call's: with G_t = lambda G_{t+1} + q_t dout_t^T, started from dstate_out,
  *   dq_t = S_t dout_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dstate_in = lambda G_0.
  * The decay is a fixed slope per head and gets no gradient. dq, dk, dv: as out. dstate_out may be
- * NULL (zeros), dstate_in may be NULL (not wanted) or dstate_out. strides: q, k, v, dout, dq, dk, dv.
+ * NULL (zeros), dstate_in may be NULL (not wanted) or dstate_out; state_in there returns
+ * FAVOR_ERR_UNSUPPORTED. strides: q, k, v, dout, dq, dk, dv.
  * An input head shared through stride 0 gets one gradient per head; their sum is the caller's.
  */
 int favor_decay_attention_backward(const void* q, const void* k, const void* v, const float* log_decay,

@@ -420,6 +420,13 @@ def _strides(*ts):
     return (_ll * len(a))(*a)
 
 
+def _dims(shape):
+    """Sizes as the C layer takes them (int)."""
+    if max(shape) > 0x7fffffff:
+        raise ValueError(f"a dimension of {tuple(shape)} exceeds 2^31 - 1")
+    return shape
+
+
 def _first(name, t, dims):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -474,7 +481,7 @@ def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None
         with on:
             return favor_decay_attention(q, k, v, log_decay, state, lengths, out, state_out, return_state)
     shape, dt = q.shape, q.dtype
-    B, H, L, d = shape
+    B, H, L, d = _dims(shape)
     if log_decay is None:
         raise TypeError("log_decay must be a float32 tensor")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
@@ -508,7 +515,7 @@ def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=
             return favor_decay_attention_backward(q, k, v, log_decay, dout, state, dstate, lengths, dq, dk, dv,
                                                   dstate_in)
     shape, dt = q.shape, q.dtype
-    B, H, L, d = shape
+    B, H, L, d = _dims(shape)
     if log_decay is None:
         raise TypeError("log_decay must be a float32 tensor")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
@@ -590,7 +597,7 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
             return favor_rotary(q, k, freq, positions, first_position, interleaved, inverse, scale, rot_scale, q_out,
                                 k_out)
     shape, dt = q.shape, q.dtype
-    B, Hq, L, d = shape
+    B, Hq, L, d = _dims(shape)
     Hk, pk, pko, wk = 0, None, None, True
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -601,6 +608,8 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
         (pk, pko), wk = _operands((B, Hk, L, d), dt, dev, k=k, k_out=k_out)
     elif k_out is not None:
         raise ValueError("k_out without k")
+    if not -0x80000000 <= first_position <= 0x7fffffff:
+        raise ValueError("first_position must fit 32 bits")
     if freq is None or freq.dim() != 1:
         raise TypeError("freq must be a float64 tensor of shape [rot/2]")
     f = _aux("freq", freq, freq.shape, torch.float64, dev)

@@ -340,8 +340,8 @@ int launch_rotary_t(favor::rot::Params p, cudaStream_t st) {
   const long long items = (long long)p.B * p.L * (p.npair + p.npass);
   const long long blocks = (items + favor::rot::kThreads - 1) / favor::rot::kThreads;
   const int heads = p.Hq + p.Hk, sms = sm_count();
-  // every head in one thread, unless that leaves fewer than four blocks an SM
-  p.groups = (int)std::max<long long>(1, std::min<long long>(heads, 4ll * sms / std::max<long long>(1, blocks)));
+  // every head in one thread, unless that leaves fewer than eight blocks an SM
+  p.groups = (int)std::max<long long>(1, std::min<long long>(heads, 8ll * sms / std::max<long long>(1, blocks)));
   p.per_group = (heads + p.groups - 1) / p.groups;
   p.groups = (heads + p.per_group - 1) / p.per_group;
   const unsigned gx = (unsigned)std::min<long long>(blocks, 64ll * sms);
@@ -417,6 +417,8 @@ int favor_decay_attention_backward(const void* q, const void* k, const void* v, 
     for (int j = 0; j < i; ++j)
       if (ptr[i] == ptr[j]) return FAVOR_ERR_UNSUPPORTED;
   }
+  // the gradient of the carried-in state may overwrite dstate_out, not the state that dq still reads
+  if (dstate_in && dstate_in == state_in) return FAVOR_ERR_UNSUPPORTED;
   if ((rc = check_device()) != FAVOR_OK) return rc;
   dcy::Params p{};
   p.s[0] = {x[1], x[2], state_in, nullptr, 0};      // S: k, v

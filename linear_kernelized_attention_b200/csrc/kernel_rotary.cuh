@@ -18,7 +18,7 @@ namespace rot {
 
 using dcy::View;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Params {
   View q, k, qy, ky;
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const Params p) {
         sn[e] = p.inverse ? -sc * s : sc * s;
       }
     }
-#pragma unroll 4
+#pragma unroll 8
     for (int h = h0; h < h1; ++h) {
       const bool isq = h < p.Hq;
       const int hh = isq ? h : h - p.Hq;

@@ -58,6 +58,7 @@ def _backward(**o):
 @pytest.mark.parametrize("over,code", COMMON + [
     ({"do": 0}, -1), ({"dq": 0}, -1), ({"dk": 0}, -1), ({"dv": 0}, -1), ({"ds": 4}, -2), ({"ds_in": 24}, -2),
     ({"L": 0}, -3), ({"dq": 16}, -5), ({"dk": 96}, -5), ({"dv": 112}, -5), ({"dv": 80}, -5),
+    ({"s_in": 160, "ds_in": 160}, -5),  # dstate_in over the state still being read
     ({"st": [OK] * 6 + [(1024, 512, 0)]}, -3), ({"st": [OK] * 4 + [(0, 512, 64)] + [OK] * 2}, -3),
 ])
 def test_backward_refuses(over, code):
@@ -111,6 +112,12 @@ def test_workspace_is_host_only():
     assert F.favor_decay_workspace_bytes(1, 1, 8, 64, 2) == 0
     assert F.favor_decay_workspace_bytes(2, 3, 1000, 40, 0) > 0
     assert F.favor_decay_workspace_bytes(2, 3, 1000, 40, 0, True) >= F.favor_decay_workspace_bytes(2, 3, 1000, 40, 0)
+
+
+def test_binding_refuses_sizes_past_int():
+    with pytest.raises(ValueError):
+        F._dims((1, 1, 2 ** 32 + 5, 8))
+    assert F._dims((2, 3, 2 ** 31 - 1, 8)) == (2, 3, 2 ** 31 - 1, 8)
 
 
 def test_binding_refuses_host_tensors():

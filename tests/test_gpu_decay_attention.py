@@ -90,6 +90,12 @@ def test_many_heads(name):
     _forward_case(20, 10, 150, 64, name, state=True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 40])
+def test_forward_segments_of_ragged_sequences(d):
+    """Few heads, long sequences: several segments a sequence, some of them behind its end."""
+    _forward_case(3, 1, 5000, d, "bf16", state=True, lengths=[5000, 1, 3071], rows="blhd", g=[-2e-3])
+
+
 def test_long_sequence_many_segments():
     _forward_case(1, 1, 9000, 64, "bf16", state=True, g=[-1e-3])
 
@@ -155,6 +161,11 @@ def test_backward_decays(g, name):
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 def test_backward_many_heads(name):
     _backward_case(20, 10, 150, 64, name, state=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_segments_of_ragged_sequences(d):
+    _backward_case(3, 1, 4500, d, "bf16", state=True, lengths=[4500, 0, 2305], rows="blhd", g=[-2e-3])
 
 
 def test_backward_long_sequence():
@@ -270,6 +281,68 @@ def test_state_in_place_and_split_prompt(name, L):
     assert float((S - ref).norm() / ref.norm()) < 2.0 ** -16
 
 
+@pytest.mark.parametrize("name,L,d", [("bf16", 300, 64), ("bf16", 6000, 64), ("bf16", 300, 128), ("f32", 500, 64),
+                                      ("bf16", 200, 20)])
+def test_gradient_state_in_place(name, L, d):
+    """dstate_in = dstate's tensor: two of the three gradients read it."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(1, 2, L, d, name)
+    S, dS = torch.randn(2, 1, 2, d, d, device="cuda")
+    ref = F.favor_decay_attention_backward(q, k, v, g, do, state=S, dstate=dS)
+    got = F.favor_decay_attention_backward(q, k, v, g, do, state=S, dstate=dS, dstate_in=dS)
+    assert got[3] is dS
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_overlapping_input_rows(d):
+    """A window sliding over one buffer: rows of an input may overlap."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(1, 2, 400, d)
+    buf = torch.randn(2, 399 * 8 + d, device="cuda").bfloat16() * 0.3
+    w = buf.as_strided((1, 2, 400, d), (0, buf.stride(0), 8, 1))
+    out, S = F.favor_decay_attention(q, w, v, g, return_state=True)
+    ref, rS = F.favor_decay_attention(q, w.contiguous(), v, g, return_state=True)
+    assert torch.equal(out, ref) and torch.equal(S, rS)
+    for a, b in zip(F.favor_decay_attention_backward(q, w, v, g, do),
+                    F.favor_decay_attention_backward(q, w.contiguous(), v, g, do)):
+        assert torch.equal(a, b)
+
+
+def test_same_tensor_as_query_key_and_value():
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, _, _, do, g = _simple(1, 2, 300, 64)
+    ref = F.favor_decay_attention(q, q.clone(), q.clone(), g, return_state=True)
+    assert all(torch.equal(a, b) for a, b in zip(F.favor_decay_attention(q, q, q, g, return_state=True), ref))
+    ref = F.favor_decay_attention_backward(q, q.clone(), q.clone(), g, do)
+    assert all(torch.equal(a, b) for a, b in zip(F.favor_decay_attention_backward(q, q, q, g, do), ref))
+
+
+def test_graphs_replayed_at_once_do_not_share_scratch():
+    """Two captured calls that each take scratch (several segments), replayed on two streams together."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    sets = [_simple(1, 1, 6000, 64, seed=s) for s in (41, 42)]
+    assert F.favor_decay_workspace_bytes(1, 1, 6000, 64) > 0
+    refs = [F.favor_decay_attention(*x[:3], x[4], return_state=True) for x in sets]
+    outs = [(torch.zeros_like(x[0]), torch.zeros(1, 1, 64, 64, device="cuda")) for x in sets]
+    torch.cuda.synchronize()
+    graphs, streams = [torch.cuda.CUDAGraph() for _ in sets], [torch.cuda.Stream() for _ in sets]
+    for gr, x, o in zip(graphs, sets, outs):
+        with torch.cuda.graph(gr):
+            F.favor_decay_attention(*x[:3], x[4], out=o[0], state_out=o[1])
+    for _ in range(5):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(refs, outs):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_repeated_calls_are_identical():
     import torch
     import linear_kernelized_attention_b200 as F
@@ -377,6 +450,9 @@ def test_refusals():
         F.favor_decay_attention(q, k, v, g, out=q[:, :1].expand_as(q).contiguous()[:, :1].expand_as(q))
     with pytest.raises(ValueError):
         F.favor_decay_attention_backward(q, k, v, g, do[:, :, :5])
+    S = torch.zeros(1, 2, 64, 64, device="cuda")
+    with pytest.raises(F.FavorError):
+        F.favor_decay_attention_backward(q, k, v, g, do, state=S, dstate_in=S)
     wide = torch.zeros(1, 1, 4, 136, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(F.FavorError) as e:
         F.favor_decay_attention(wide, wide, wide, g[:1])

@@ -109,6 +109,8 @@ def test_refusals():
         F.favor_rotary(q, None, freq, positions=torch.zeros(8, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         F.favor_rotary(q, None, freq, k_out=q)
+    with pytest.raises(ValueError):
+        F.favor_rotary(q, None, freq, first_position=2 ** 31)
     with pytest.raises(F.FavorError):
         F.favor_rotary(q, None, torch.ones(33, dtype=torch.float64, device="cuda"))
     with pytest.raises(F.FavorError):
