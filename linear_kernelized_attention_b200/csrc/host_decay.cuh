@@ -174,6 +174,8 @@ bool tc_view_ok(const View& v) {
   return true;
 }
 
+// Everything they can read goes to the tensor cores. Measured against the CUDA-core route on the device, 8 heads,
+// d = 64: one token 5.8 and 13.0 us, 128 tokens 6.0 and 27.5; 128 heads x 512 tokens of d = 128 16 and 380.
 bool tc_route(const dcy::Params& p, int dtype_code) {
   if (dtype_code != 1 || p.d % 8 != 0) return false;
   for (int i = 0; i < p.nouts; ++i)
@@ -320,9 +322,10 @@ template <typename T>
 int launch_decay_step(const dcy::StepParams& p0, int BH, int d, cudaStream_t st) {
   dcy::StepParams p = p0;
   const bool vec = d % 4 == 0;
-  // Slices of 32 columns (whole 128-byte row pieces) while all heads' slices are below two blocks
-  // an SM, else whole rows.
-  p.cols = d <= 32 || (long long)BH * ((d + 31) / 32) > 2ll * sm_count() ? d : 32;
+  // Slices of 32 columns (whole 128-byte row pieces) while all heads' slices are one block an SM at most, else
+  // whole rows. Measured, slices against whole rows: 8 heads of d = 64 2.49 and 2.56 us, 32 heads of d = 128 2.99
+  // and 3.99; past an SM each, 128 heads of d = 64 3.05 and 2.79, 4096 heads 34.2 and 20.2.
+  p.cols = d <= 32 || (long long)BH * ((d + 31) / 32) > sm_count() ? d : 32;
   p.slices = (d + p.cols - 1) / p.cols;
   if ((long long)BH * p.slices > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)((long long)BH * p.slices);
@@ -340,7 +343,8 @@ int launch_rotary_t(favor::rot::Params p, cudaStream_t st) {
   const long long items = (long long)p.B * p.L * (p.npair + p.npass);
   const long long blocks = (items + favor::rot::kThreads - 1) / favor::rot::kThreads;
   const int heads = p.Hq + p.Hk, sms = sm_count();
-  // every head in one thread, unless that leaves fewer than eight blocks an SM
+  // every head in one thread, unless that leaves fewer than eight blocks an SM. Measured at 4 x 4096 tokens of 16
+  // heads: 2 groups 13.7 us, 4 groups 15.9, 8 groups 18.2; one token of 64 sequences and 20 heads: 20 groups 2.8
   p.groups = (int)std::max<long long>(1, std::min<long long>(heads, 8ll * sms / std::max<long long>(1, blocks)));
   p.per_group = (heads + p.groups - 1) / p.groups;
   p.groups = (heads + p.per_group - 1) / p.per_group;
@@ -353,7 +357,8 @@ int launch_rotary_t(favor::rot::Params p, cudaStream_t st) {
 template <typename T>
 int launch_rotary(const favor::rot::Params& p, int interleaved, bool strides_ok, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  // 16-byte pieces where every row starts on one and the pairs and the rest fill whole ones
+  // 16-byte pieces where every row starts on one and the pairs and the rest fill whole ones, else single
+  // elements, which take any row
   const bool vec = strides_ok && (p.rot / 2) % V == 0 && (p.d - p.rot) % V == 0;
   if (interleaved) return vec ? launch_rotary_t<T, V, true>(p, st) : launch_rotary_t<T, 1, true>(p, st);
   return vec ? launch_rotary_t<T, V, false>(p, st) : launch_rotary_t<T, 1, false>(p, st);

@@ -23,10 +23,11 @@
 // d <= 128 accumulates hi, then lo.
 //
 // What bounds it. An SM's share of HBM delivers a d = 64 chunk in about 2700 cycles and a d = 128 one in
-// 5400; a chunk takes about 2950 and 5550. Shared memory is the busiest unit beside it (the MMAs' operands,
-// the loads, w B in place, the image: about 2300 of its 128-byte cycles a d = 64 chunk). Long sequences of
-// few heads are cut into segments: the state kernel sums each segment's own state from b and c alone,
-// k_chunk_scan carries them, and this kernel walks all segments at once.
+// 5400; a chunk takes about 3000 and 5500 (measured: 16 heads x 65536 tokens, d = 64, in 98 us). The
+// products themselves take 1100 and 2300 of them; shared memory is busy for about 2300 at d = 64 (operands of
+// the MMAs, loads, w B in place, the image), and each role's instructions and hand-overs for 1000 to 1600.
+// Long sequences of few heads are cut into segments: the state kernel sums each segment's own state from
+// b and c alone, k_chunk_scan carries them, and this kernel walks all segments at once.
 //
 // Warps: 0 TMA; 1 TMEM allocation and every MMA; 4-11 w B and state; 12-19 scores; 20-27
 // rows out. Thread = row of its 128 (token or state row).

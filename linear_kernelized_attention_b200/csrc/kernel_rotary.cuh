@@ -9,7 +9,9 @@
 //
 // Reading and writing q and k bounds it. One thread computes the sines of V pairs of one token once
 // and applies them to every head of its head group (q's heads, then k's), several heads' loads in
-// flight; heads are split into groups only where there are too few tokens to fill the GPU.
+// flight; heads are split into groups only where there are too few tokens to fill the GPU. Measured: 4 x 4096
+// tokens of 8 + 8 heads of 64 columns in 13.7 us, 4900 GB/s (75% of a plain copy); twice as many groups, each
+// with the sines again, 15.9 us, and sines shared through shared memory 17.9 us.
 #pragma once
 #include "kernels_decay.cuh"
 

@@ -1,5 +1,5 @@
 // kernels_decay.cuh - causal linear attention with one decay per head, and its gradients, on CUDA
-// cores in fp32: every type, head size and stride the entry points take.
+// cores in fp32: fp32 operands, and bf16 ones whose rows are not whole 16-byte pieces.
 //
 // What it computes. With lambda = exp(log_decay[h]) and, for every (batch, head),
 //   S_t = lambda S_{t-1} + k_t v_t^T,   out_t = S_t^T q_t          (S_{-1} = state_in or 0)
@@ -19,6 +19,10 @@
 // Three launches: chunk updates (every chunk at once), the scan over chunks (one thread per state
 // element, in double), the outputs (every chunk at once). Powers of lambda are evaluated in double:
 // the library is built with fast single-precision intrinsics.
+//
+// Three launches overlap through programmatic dependent launch. Measured: fp32 prompts of 2 x 8 heads x 1023
+// tokens, d = 64, in 32.8 us (update 9, scan 7, outputs 20 alone), gradients of 8 heads x 777 tokens in 32.9;
+// bound by fp32 FMA from shared memory at 256 to 312 blocks. Scalar shared reads took 73 us.
 //
 // A product whose weight the mask removes is never formed (it is skipped, not multiplied by zero),
 // so infinities and NaN in later tokens do not reach earlier rows. Tokens at and past the sequence's
