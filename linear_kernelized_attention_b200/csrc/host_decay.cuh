@@ -139,8 +139,8 @@ int launch_decay_cc(dcy::Params p, int dtype_code, cudaStream_t st) {
 
 // ------------------------------------------------------------------ tensor-core route
 // How a call's walk is cut: chunks per segment, segments. `scan` (several segments): segment states,
-// their scan and the walk, three launches; else one walk per head from the carried-in state, and beside it
-// the states a caller wants back.
+// their scan and the walk, three launches; else one walk per head from the carried-in state, and the states a
+// caller wants back.
 struct WalkPlan {
   int cps, nseg;
   bool scan;
@@ -220,11 +220,14 @@ struct OperandMaps {
   }
 };
 
+void set_maps(const OperandMaps& om, CUtensorMap* m, int* bm, int* hm) {
+  std::copy(om.m, om.m + 4, m);
+  std::copy(om.bm, om.bm + 4, bm);
+  std::copy(om.hm, om.hm + 4, hm);
+}
+
 // The states in p.s that have a use: every segment's (ws), or the whole sequences' written to their `out`.
-template <int DP>
-int launch_states(const dcy::Params& p, OperandMaps& om, float* ws, int nseg, int cps, bool beside, cudaStream_t st) {
-  using C = dst::Cfg<DP>;
-  dst::Params sp{};
+int state_params(dst::Params& sp, const dcy::Params& p, OperandMaps& om, float* ws, int nseg, int cps) {
   for (int i = 0; i < p.nstates; ++i) {
     if (!ws && !p.s[i].out) continue;
     dst::Job& j = sp.j[sp.njobs++];
@@ -235,23 +238,15 @@ int launch_states(const dcy::Params& p, OperandMaps& om, float* ws, int nseg, in
     j.in = p.s[i].in;
     j.out = p.s[i].out;
   }
-  if (!sp.njobs) return FAVOR_OK;
-  std::copy(om.m, om.m + 4, sp.m);
-  std::copy(om.bm, om.bm + 4, sp.bm);
-  std::copy(om.hm, om.hm + 4, sp.hm);
+  set_maps(om, sp.m, sp.bm, sp.hm);
   sp.ws = ws;
   sp.log_decay = p.log_decay;
   sp.lengths = p.lengths;
   sp.B = p.B, sp.H = p.H, sp.L = p.L, sp.d = p.d, sp.nseg = nseg, sp.cps = cps;
-  auto k = dst::k_decay_state<DP>;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(k), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
-  return launch_with<dst::Params>(k, (long long)p.B * p.H * nseg * sp.njobs, C::kThreads, C::kSmem, st, beside, sp);
+  return FAVOR_OK;
 }
 
-template <int DP>
-int launch_walk(const dcy::Params& p, OperandMaps& om, const float* ws, const WalkPlan& pl, cudaStream_t st) {
-  using C = dtc::Cfg<DP>;
-  dtc::Params tp{};
+int walk_params(dtc::Params& tp, const dcy::Params& p, OperandMaps& om, const float* ws, const WalkPlan& pl) {
   tp.njobs = p.nouts;
   for (int i = 0; i < p.nouts; ++i) {
     dtc::Job& j = tp.j[i];
@@ -266,35 +261,56 @@ int launch_walk(const dcy::Params& p, OperandMaps& om, const float* ws, const Wa
     int bm, hm;
     if (!make_map_view(&tp.my[i], &bm, &hm, j.y, p.B, p.H, p.L, p.d, true)) return FAVOR_ERR_CUDA;
   }
-  std::copy(om.m, om.m + 4, tp.m);
-  std::copy(om.bm, om.bm + 4, tp.bm);
-  std::copy(om.hm, om.hm + 4, tp.hm);
+  set_maps(om, tp.m, tp.bm, tp.hm);
   for (int i = 0; i < p.nstates; ++i) tp.in[i] = p.s[i].in;
   tp.ws = ws;
   tp.log_decay = p.log_decay;
   tp.lengths = p.lengths;
   tp.B = p.B, tp.H = p.H, tp.L = p.L, tp.d = p.d, tp.nseg = pl.nseg, tp.cps = pl.cps;
-  auto k = dtc::k_decay_walk<DP>;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(k), C::kSmem) != FAVOR_OK) return FAVOR_ERR_CUDA;
-  return launch_with<dtc::Params>(k, (long long)p.B * p.H * pl.nseg * p.nouts, C::kThreads, C::kSmem, st, pl.scan, tp);
+  return FAVOR_OK;
+}
+
+template <typename P>
+int launch_blocks(void (*k)(P), long long grid, int threads, int smem, bool pdl, const P& p, cudaStream_t st) {
+  if (ensure_smem_attr(reinterpret_cast<const void*>(k), smem) != FAVOR_OK) return FAVOR_ERR_CUDA;
+  return launch_with<P>(k, grid, threads, smem, st, pdl, p);
 }
 
 template <int DP>
 int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaStream_t st) {
-  if ((long long)p.B * p.H * pl.nseg * 3 > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
+  using WC = dtc::Cfg<DP>;
+  using SC = dst::Cfg<DP>;
+  const long long heads = (long long)p.B * p.H;
+  if (heads * pl.nseg * 5 > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
   OperandMaps om;
-  int rc = FAVOR_OK;
-  if (pl.scan) {
-    rc = launch_states<DP>(p, om, ws, pl.nseg, pl.cps, false, st);
-    if (rc == FAVOR_OK) rc = launch_scan(p, ws, pl.nseg, pl.cps * dtc::kTok, st);
-    return rc == FAVOR_OK ? launch_walk<DP>(p, om, ws, pl, st) : rc;
-  }
-  rc = launch_walk<DP>(p, om, nullptr, pl, st);
+  dst::Both both{};
+  dtc::Params& tp = both.w;
+  dst::Params& sp = both.s;
+  int rc = walk_params(tp, p, om, ws, pl);
+  if (rc == FAVOR_OK) rc = state_params(sp, p, om, ws, pl.nseg, pl.cps);
   if (rc != FAVOR_OK) return rc;
-  // the whole sequences' states: beside the walk, or after it where they overwrite what it reads
-  bool beside = true;
-  for (int i = 0; i < p.nstates; ++i) beside = beside && !(p.s[i].out && p.s[i].out == p.s[i].in);
-  return launch_states<DP>(p, om, nullptr, 1, pl.cps, beside, st);
+  set_maps(om, tp.m, tp.bm, tp.hm);
+  const long long nwalk = heads * pl.nseg * p.nouts, nstate = heads * pl.nseg * sp.njobs;
+  if (pl.scan) {
+    rc = launch_blocks(dst::k_decay_state<DP>, nstate, SC::kThreads, SC::kSmem, false, sp, st);
+    if (rc == FAVOR_OK) rc = launch_scan(p, ws, pl.nseg, pl.cps * dtc::kTok, st);
+    if (rc == FAVOR_OK) rc = launch_blocks(dtc::k_decay_walk<DP>, nwalk, WC::kThreads, WC::kSmem, true, tp, st);
+    return rc;
+  }
+  if (!sp.njobs) return launch_blocks(dtc::k_decay_walk<DP>, nwalk, WC::kThreads, WC::kSmem, false, tp, st);
+  // The whole sequences' states: in the walk's own launch where the call is short (one block an SM, eight chunks
+  // at most), since the second launch costs the host 3 us (8 heads x 256 tokens of d = 64: 15.9 us in two launches, 14.5
+  // in one) but the joint kernel's registers slow a long walk (24 heads x 2049 tokens of d = 128: 61.5 us and 64.9);
+  // else beside it, or after it where they overwrite what it reads.
+  bool in_place = false;
+  for (int i = 0; i < p.nstates; ++i) in_place = in_place || (p.s[i].out && p.s[i].out == p.s[i].in);
+  if (!in_place && nwalk + nstate <= sm_count() && pl.cps <= 8) {
+    both.nwalk = (int)nwalk;
+    return launch_blocks(dst::k_decay_both<DP>, nwalk + nstate, WC::kThreads, std::max(WC::kSmem, SC::kSmem), false,
+                         both, st);
+  }
+  rc = launch_blocks(dtc::k_decay_walk<DP>, nwalk, WC::kThreads, WC::kSmem, false, tp, st);
+  return rc == FAVOR_OK ? launch_blocks(dst::k_decay_state<DP>, nstate, SC::kThreads, SC::kSmem, !in_place, sp, st) : rc;
 }
 
 int launch_decay_tc(const dcy::Params& p, cudaStream_t st) {

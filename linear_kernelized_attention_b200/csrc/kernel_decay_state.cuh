@@ -23,7 +23,7 @@
 // buffer d = 128 took 3.2 us, and units of 64 tokens at d = 64 took 1.6.
 //
 // Warps: 0 TMA; 1 TMEM allocation and MMAs; 4-11 the three terms of w b (hi in place, mid and lo beside
-// it); 12-15 (d <= 64) or 12-19 the running sums, thread = row of X (b's column).
+// it); from 12 on the running sums, thread = row of X (b's column).
 // d <= 64: [hi; mid] as the 128 rows of one operand, [lo; mid] as another whose second half is unused.
 #pragma once
 #include "kernel_decay_tc.cuh"
@@ -76,8 +76,11 @@ struct Misc {
   uint64_t full[4], empty[4], t_full[2], t_free[2], done[2], d_free[2], sync, drain;
 };
 
-template <int DP>
-__global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __grid_constant__ Params p) {
+// The state of block `block`: job, segment and head. SC: columns a thread sums, 64, or 32 where the block has the
+// walk's many threads and few registers each.
+template <int DP, int SC>
+__device__ __forceinline__ void state_block(const Params& p, unsigned block) {
+  constexpr int kSumWarps = 4 * DP / SC;
   using C = Cfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -91,9 +94,9 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
   // counters and MMA descriptors then live in uniform registers (otherwise an MMA takes 100 to 150 cycles to
   // issue; the products themselves take 32 to 64).
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int jid = blockIdx.x % p.njobs;
-  const int seg = (blockIdx.x / p.njobs) % p.nseg;
-  const int bh = blockIdx.x / p.njobs / p.nseg;
+  const int jid = block % p.njobs;
+  const int seg = (block / p.njobs) % p.nseg;
+  const int bh = block / p.njobs / p.nseg;
   const int b = bh / p.H, h = bh % p.H;
   const Job& job = p.j[jid];
   const int rev = job.reverse, d = p.d;
@@ -131,9 +134,9 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(ms->done[s]), 1);
-      mbar_init(bar(ms->d_free[s]), DP / 16);
+      mbar_init(bar(ms->d_free[s]), kSumWarps);
     }
-    mbar_init(bar(ms->sync), 128);
+    mbar_init(bar(ms->sync), 32 * kSumWarps);
     mbar_init(bar(ms->drain), 1);
     fence_mbar_init();
     for (int i = 0; i < min(N, C::NS); ++i) load(i);  // in flight while the block sets up
@@ -255,21 +258,21 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ms->t_full[tb]));
     }
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ running sums (thread = row of X, 64 columns)
-    const int q4 = warp & 3, row = q4 * 32 + lane, col0 = DP > 64 ? 64 * ((warp - 12) >> 2) : 0;
+  } else if (warp >= 12 && warp < 12 + kSumWarps) {
+    // ------------------------------------------------------------ running sums (thread = row of X, SC columns)
+    const int q4 = warp & 3, row = q4 * 32 + lane, col0 = SC * ((warp - 12) >> 2);
     const uint32_t la = uint32_t(q4 * 32) << 16;
     const bool second = DP > 64 || q4 < 2;  // d <= 64: rows 64.. of the second accumulator are unused
-    float x[64];
+    float x[SC];
 #pragma unroll
-    for (int e = 0; e < 64; ++e) x[e] = 0.f;
+    for (int e = 0; e < SC; ++e) x[e] = 0.f;
     bool ok = true;
     for (int i = 0; i < N; ++i) {
       if (!(ok = mbar_wait(bar(ms->done[i & 1]), (i >> 1) & 1, abort_flag))) break;
       tc_fence_after();
       const uint32_t acc = tmem + la + (i & 1) * C::kAcc + col0;
 #pragma unroll
-      for (int y = 0; y < 64; y += 8) {
+      for (int y = 0; y < SC; y += 8) {
         uint32_t v[8], u[8];
         if (second) tmem_ld8(acc + DP + y, v);
         tmem_ld8(acc + y, u);
@@ -291,12 +294,12 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
       ok = __all_sync(0xffffffffu, ok);
       if (ok && row >= 64) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) scr[e * 64 + row - 64] = x[e];
+        for (int e = 0; e < SC; ++e) scr[(col0 + e) * 64 + row - 64] = x[e];
       }
       ok = group_sync(bar(ms->sync), ph, abort_flag) && ok;
       if (ok && row < 64) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] += scr[e * 64 + row];
+        for (int e = 0; e < SC; ++e) x[e] += scr[(col0 + e) * 64 + row];
       }
     }
     if (ok && row < d && row < DP && (DP > 64 || row < 64)) {
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
       const float* in = !p.ws && job.in ? job.in + bh * dd : nullptr;
       const double f = in ? dcy::decay_pow(p.log_decay[h], len) : 0.0;
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) {
+      for (int e = 0; e < SC; e += 4) {
         if (col0 + e >= d) continue;
         const long long at = (long long)row * d + col0 + e;
         float4 y = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
@@ -325,7 +328,27 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __gr
     tc_fence_after();
     tmem_dealloc(ms->tmem_base, C::kCols);
   }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_state(const __grid_constant__ Params p) {
+  state_block<DP, 64>(p, blockIdx.x);
   pdl_wait();  // where this kernel was started beside the walk: it ends after it
+}
+
+// Walks and, in the blocks behind them, the whole sequences' states, in one launch for short calls. The blocks
+// share nothing.
+struct Both {
+  dtc::Params w;
+  Params s;
+  int nwalk;
+};
+template <int DP>
+__global__ void __launch_bounds__(dtc::Cfg<DP>::kThreads, 1) k_decay_both(const __grid_constant__ Both p) {
+  if ((int)blockIdx.x < p.nwalk)
+    dtc::walk_block<DP>(p.w, blockIdx.x);
+  else
+    state_block<DP, 32>(p.s, blockIdx.x - p.nwalk);
 }
 
 }  // namespace dst

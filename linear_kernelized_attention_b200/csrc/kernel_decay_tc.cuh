@@ -204,8 +204,9 @@ __device__ __forceinline__ void load_state(uint32_t (&v)[32], const float* in, i
   }
 }
 
+// The walk of block `block`: job, segment and head.
 template <int DP>
-__global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __grid_constant__ Params p) {
+__device__ __forceinline__ void walk_block(const Params& p, unsigned block) {
   using C = Cfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -219,9 +220,9 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
   // counters and MMA descriptors then live in uniform registers (otherwise an MMA takes 100 to 150 cycles to
   // issue; the products themselves take 32 to 64).
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int jid = blockIdx.x % p.njobs;
-  const int seg = (blockIdx.x / p.njobs) % p.nseg;
-  const int bh = blockIdx.x / p.njobs / p.nseg;
+  const int jid = block % p.njobs;
+  const int seg = (block / p.njobs) % p.nseg;
+  const int bh = block / p.njobs / p.nseg;
   const int b = bh / p.H, h = bh % p.H;
   const Job& job = p.j[jid];
   const int rev = job.reverse, d = p.d;
@@ -717,6 +718,11 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __gri
     tc_fence_after();
     tmem_dealloc(ms->tmem_base, C::kCols);
   }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(Cfg<DP>::kThreads, 1) k_decay_walk(const __grid_constant__ Params p) {
+  walk_block<DP>(p, blockIdx.x);
 }
 
 }  // namespace dtc
