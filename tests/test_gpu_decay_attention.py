@@ -311,6 +311,28 @@ def test_overlapping_input_rows(d):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("name,d", [("bf16", 64), ("bf16", 20), ("f32", 64)])
+def test_offsets_past_32_bits(name, d):
+    """Batch entries more than 2^32 bytes apart, inputs and outputs."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    dt = _dtype(name)
+    far = (2 ** 32 // torch.empty((), dtype=dt).element_size()) + 64
+    big = [torch.empty(far + 200 * d, dtype=dt, device="cuda") for _ in range(2)]
+    x, o = (b.as_strided((2, 1, 200, d), (far, 200 * d, d, 1)) for b in big)
+    q = _simple(2, 1, 200, d, name)[0]
+    x.copy_(q)
+    g = torch.tensor([-0.05], device="cuda")
+    ref, rS = F.favor_decay_attention(q, q, q, g, return_state=True)
+    out, S = F.favor_decay_attention(x, x, x, g, out=o, return_state=True)
+    assert torch.equal(out, ref) and torch.equal(S, rS)
+    rg = F.favor_decay_attention_backward(q, q, q, g, q)
+    assert torch.equal(F.favor_decay_attention_backward(x, x, x, g, x, dq=o)[0], rg[0])
+    freq, _ = F.favor_rotary_frequencies(d, device="cuda")
+    F.favor_rotary(x, None, freq, q_out=o)
+    assert torch.equal(o, F.favor_rotary(q, None, freq)[0])
+
+
 def test_same_tensor_as_query_key_and_value():
     import torch
     import linear_kernelized_attention_b200 as F

@@ -69,6 +69,21 @@ def test_steps_equal_prompt():
     assert (np.abs(S.double().cpu().numpy() - refS) <= (4 + 2 * T) * C.U32 * magS).all()
 
 
+def test_step_state_past_32_bit_offsets():
+    """More than 2^31 state elements: the last heads as a small call gives them."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    B, H, d = 1030, 128, 128
+    S = torch.zeros(B, H, d, d, device="cuda")
+    S[-1].normal_()
+    q, k, v = (torch.randn(B, H, d, device="cuda").bfloat16() for _ in range(3))
+    g = torch.full((H,), -0.1, device="cuda")
+    last = S[-1:].clone()
+    out = F.favor_decay_step(q, k, v, g, S)
+    ref = F.favor_decay_step(q[-1:], k[-1:], v[-1:], g, last)
+    assert torch.equal(S[-1:], last) and torch.equal(out[-1:], ref)
+
+
 def test_step_in_a_graph_advances_the_state():
     import torch
     import linear_kernelized_attention_b200 as F
