@@ -379,37 +379,41 @@ def favor_attention_backward_f32(q, k, v, omega, dout, feature_kind=FAVOR_TRIG, 
 # ---------------------------------------------------------------- linear attention with a decay
 # A single-token call costs a few microseconds on the device, so the checks below stay on the few
 # attributes that decide, and errors are worded only once one fails.
-def _operands(shape, dtype, device, **ts):
+def _operands(shape, dtype, device, names, *ts):
     """Pointers of operands [B, H, L, d] (or [B, H, d]) read in place (any strides, d contiguous), and whether
     all are contiguous."""
-    ptrs, whole = [], True
-    for name, t in ts.items():
-        try:
-            if t.dtype is dtype and t.shape == shape and t.device == device:
-                if not t.is_contiguous():
-                    whole = False
-                    if t.stride(-1) != 1 and shape[-1] > 1:
-                        raise ValueError(f"{name} must be contiguous in its last dimension")
-                ptrs.append(t.data_ptr())
-                continue
-        except AttributeError:
-            raise TypeError(f"{name} must be a CUDA tensor") from None
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
-    return ptrs, whole
+    ptrs, whole, index = [], True, device.index
+    try:
+        for t in ts:
+            if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+                break
+            if not t.is_contiguous():
+                whole = False
+                if t.stride(-1) != 1 and shape[-1] > 1:
+                    raise ValueError(f"{names[len(ptrs)]} must be contiguous in its last dimension")
+            ptrs.append(t.data_ptr())
+        else:
+            return ptrs, whole
+    except AttributeError:
+        raise TypeError(f"{names[len(ptrs)]} must be a CUDA tensor") from None
+    name = names[len(ptrs)]
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
 
 
 def _aux(name, t, shape, dtype, device):
     """A contiguous companion tensor (decays, lengths, states, positions), or None."""
-    import torch
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == device.index:
+            if t.shape == shape and t.is_contiguous():
+                return t.data_ptr()
+            raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    except AttributeError:
+        pass
+    raise TypeError(f"{name} must be a {dtype} tensor on {device}")
 
 
 def _strides(*ts):
@@ -489,7 +493,7 @@ def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None
     n = _aux("lengths", lengths, (B,), torch.int32, dev)
     if out is None:
         out = _new(q, lengths is not None)
-    (pq, pk, pv, po), whole = _operands(shape, dt, dev, q=q, k=k, v=v, out=out)
+    (pq, pk, pv, po), whole = _operands(shape, dt, dev, ("q", "k", "v", "out"), q, k, v, out)
     if state_out is None and return_state:
         state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
     s_out = _aux("state_out", state_out, (B, H, d, d), torch.float32, dev)
@@ -524,7 +528,8 @@ def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=
     n = _aux("lengths", lengths, (B,), torch.int32, dev)
     zero = lengths is not None
     dq, dk, dv = (_new(q, zero) if t is None else t for t in (dq, dk, dv))
-    (pq, pk, pv, pdo, pdq, pdk, pdv), whole = _operands(shape, dt, dev, q=q, k=k, v=v, dout=dout, dq=dq, dk=dk, dv=dv)
+    (pq, pk, pv, pdo, pdq, pdk, pdv), whole = _operands(shape, dt, dev, ("q", "k", "v", "dout", "dq", "dk", "dv"),
+                                                        q, k, v, dout, dq, dk, dv)
     if dstate_in is None and (state is not None or dstate is not None):
         dstate_in = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
     ds_in = _aux("dstate_in", dstate_in, (B, H, d, d), torch.float32, dev)
@@ -555,7 +560,7 @@ def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
     s = _aux("state", state, (B, H, d, d), torch.float32, dev)
     if out is None:
         out = _new(q, False)
-    (pq, pk, pv, po), whole = _operands(shape, dt, dev, q=q, k=k, v=v, out=out)
+    (pq, pk, pv, po), whole = _operands(shape, dt, dev, ("q", "k", "v", "out"), q, k, v, out)
     rc = lib().favor_decay_step(pq, pk, pv, g, s, po, B, H, d, code, None if whole else _strides(q, k, v, out),
                                 _handle(dev))
     if rc != 0:
@@ -605,7 +610,7 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
         Hk = k.shape[1]
         if k_out is None:
             k_out = _new(k, False)
-        (pk, pko), wk = _operands((B, Hk, L, d), dt, dev, k=k, k_out=k_out)
+        (pk, pko), wk = _operands((B, Hk, L, d), dt, dev, ("k", "k_out"), k, k_out)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if not -0x80000000 <= first_position <= 0x7fffffff:
@@ -616,7 +621,7 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
     pos = _aux("positions", positions, (B, L), torch.int32, dev)
     if q_out is None:
         q_out = _new(q, False)
-    (pq, pqo), wq = _operands(shape, dt, dev, q=q, q_out=q_out)
+    (pq, pqo), wq = _operands(shape, dt, dev, ("q", "q_out"), q, q_out)
     rc = lib().favor_rotary(pq, pk, f, pos, pqo, pko, B, Hq, Hk, L, d, 2 * freq.shape[0], int(interleaved), int(inverse),
                             int(first_position), scale, rot_scale, code,
                             None if wq and wk else _strides(q, k, q_out, k_out), _handle(dev))
