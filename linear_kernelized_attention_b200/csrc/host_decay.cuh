@@ -99,7 +99,11 @@ int launch_scan(const dcy::Params& p, float* ws, int nseg, int seg, cudaStream_t
   sp.nstates = p.nstates, sp.B = p.B, sp.H = p.H, sp.L = p.L, sp.d = p.d, sp.nseg = nseg, sp.seg = seg;
   const long long grid = (long long)p.B * p.H * p.nstates * ((p.d * p.d + dcy::kThreads - 1) / dcy::kThreads);
   if (grid > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
-  return launch_with(dcy::k_chunk_scan, grid, dcy::kThreads, 0, st, true, sp);
+  // 32 segments' loads in flight where there are many, 8 (a third of the registers, so more blocks an SM) where few.
+  // Measured, fp32 calls of d = 64, 8 against 32: one head of 1024 segments 191 and 166 us, 16 heads of 128 segments 162
+  // and 150; 16 heads of 16 segments 29.9 and 31.1, 256 heads of 2 segments 52 and 83.
+  return nseg >= 64 ? launch_with<dcy::ScanParams>(dcy::k_chunk_scan<32>, grid, dcy::kThreads, 0, st, true, sp)
+                    : launch_with<dcy::ScanParams>(dcy::k_chunk_scan<8>, grid, dcy::kThreads, 0, st, true, sp);
 }
 
 template <typename T, int DP>

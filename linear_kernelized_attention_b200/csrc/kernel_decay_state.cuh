@@ -17,8 +17,8 @@
 // beyond it, grows from 1 by one product (in double) a chunk, and nothing is ever rescaled.
 //
 // Reading b and c bounds it at best: 32 KB a chunk and head at d = 64, 1400 cycles of an SM's share of HBM.
-// Measured: 1.3 us (2300 cycles) a chunk at d = 64 and 2.0 at d = 128, most of it the issue of the products,
-// whose own time is 770 and 1540 cycles. Terms are made in units of 8192 elements (128 tokens, or 64 at
+// Measured: 1.3 us (2300 cycles) a chunk at d = 64 and 2.0 at d = 128, most of it the products, which alone
+// take 770 and 1540 cycles. Terms are made in units of 8192 elements (128 tokens, or 64 at
 // d > 64) with two buffers, so that one unit's products run beside the next one's arithmetic; with one
 // buffer d = 128 took 3.2 us, and units of 64 tokens at d = 64 took 1.6.
 //

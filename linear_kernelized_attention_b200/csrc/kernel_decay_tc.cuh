@@ -23,7 +23,7 @@
 // d <= 128 accumulates hi, then lo.
 //
 // What bounds it. An SM's share of HBM delivers a d = 64 chunk in about 2700 cycles and a d = 128 one in
-// 5400; a chunk takes about 3000 and 5500 (measured: 16 heads x 65536 tokens, d = 64, in 98 us). The
+// 5400; a chunk takes 2600 to 3000 and 5500 (measured: 16 heads x 65536 tokens, d = 64, in 98 us). The
 // products themselves take 1100 and 2300 of them; shared memory is busy for about 2300 at d = 64 (operands of
 // the MMAs, loads, w B in place, the image), and each role's instructions and hand-overs for 1000 to 1600.
 // Long sequences of few heads are cut into segments: the state kernel sums each segment's own state from

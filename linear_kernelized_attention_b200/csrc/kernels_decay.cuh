@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(kThreads) k_chunk_update(const __grid_constant
 
 // Each segment's update (p.seg tokens; a chunk is one) replaced by the state it is handed; the
 // boundary states read and written. One thread per (state job, head, element); the running state is
-// held in double. Eight segments' loads are in flight at a time: the chain itself is one fma a segment.
-static __global__ void __launch_bounds__(kThreads) k_chunk_scan(const __grid_constant__ ScanParams p) {
-  constexpr int G = 8;
+// held in double. G segments' loads are in flight at a time: the chain itself is one fma a segment.
+template <int G>
+__global__ void __launch_bounds__(kThreads) k_chunk_scan(const __grid_constant__ ScanParams p) {
   __shared__ double pw[2];  // lambda^seg, lambda^(tokens of the last segment)
   const int dd = p.d * p.d, nb = (dd + kThreads - 1) / kThreads;
   const int q = blockIdx.x / nb, el = (blockIdx.x % nb) * kThreads + threadIdx.x;
