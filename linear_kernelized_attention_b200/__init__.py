@@ -615,7 +615,7 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
         raise ValueError("k_out without k")
     if not -0x80000000 <= first_position <= 0x7fffffff:
         raise ValueError("first_position must fit 32 bits")
-    if freq is None or freq.dim() != 1:
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
         raise TypeError("freq must be a float64 tensor of shape [rot/2]")
     f = _aux("freq", freq, freq.shape, torch.float64, dev)
     pos = _aux("positions", positions, (B, L), torch.int32, dev)

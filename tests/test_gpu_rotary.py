@@ -102,6 +102,8 @@ def test_refusals():
     with pytest.raises(TypeError):
         F.favor_rotary(q, q, freq.float())
     with pytest.raises(TypeError):
+        F.favor_rotary(q, q, [1.0] * 16)
+    with pytest.raises(TypeError):
         F.favor_rotary(q, q.bfloat16(), freq)
     with pytest.raises(TypeError):
         F.favor_rotary(q, None, freq, positions=torch.zeros(1, 8, dtype=torch.int64, device="cuda"))
