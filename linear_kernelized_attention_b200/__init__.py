@@ -451,8 +451,8 @@ def _elsewhere(device, stream):
         if torch._C._cuda_getDevice() == device.index:
             return None
         return torch.cuda.device(device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+    if isinstance(stream, int):  # 0 is the default stream; torch would wrap it as a new stream of its pool
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"stream of {stream.device} for tensors on {device}")
     return torch.cuda.stream(stream)

@@ -132,3 +132,17 @@ def test_binding_refuses_host_tensors():
         F.favor_decay_step(x[:, :, 0], x[:, :, 0], x[:, :, 0], g, torch.zeros(1, 1, 8, 8))
     with pytest.raises(TypeError):
         F.favor_rotary(x, x, torch.zeros(4, dtype=torch.float64))
+
+
+def test_stream_handle_zero_is_the_default_stream(monkeypatch):
+    """torch.cuda.current_stream().cuda_stream is 0 on the default stream; wrapped as an external stream, 0 gives
+    another stream of torch's pool, which runs beside the caller's work."""
+    import types
+
+    import torch
+    dev = torch.device("cuda", 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: types.SimpleNamespace(device=device, of=h))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: types.SimpleNamespace(device=device, of="default"))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert F._elsewhere(dev, 0).of == "default"
+    assert F._elsewhere(dev, 64).of == 64

@@ -182,3 +182,21 @@ def test_rotary_feeds_favor_attention_and_its_decode():
                                 feature_kind=F.FAVOR_RELU)
         e = (o.float() - ref[:, :, t].float()).abs().amax(-1) / ref[:, :, t].float().abs().amax(-1)
         assert float(e.max()) < 2e-2 + 5e-3
+
+
+def test_stream_handle_of_the_default_stream():
+    """Handle 0: the call runs on the default stream itself, behind the work already there."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    dev = torch.device("cuda", torch.cuda.current_device())
+    assert torch.cuda.default_stream().cuda_stream == 0
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with F._elsewhere(dev, 0):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    with F._elsewhere(dev, torch.cuda.current_stream().cuda_stream):
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    q, k, v = (torch.randn(2, 4, 64, device="cuda") for _ in range(3))
+    g = torch.from_numpy(C.slopes(4)).cuda()
+    S, ref = torch.zeros(2, 2, 4, 64, 64, device="cuda")
+    want = F.favor_decay_step(q, k, v, g, ref)
+    assert torch.equal(F.favor_decay_step(q, k, v, g, S, stream=0), want) and torch.equal(S, ref)
