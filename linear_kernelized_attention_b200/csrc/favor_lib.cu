@@ -174,7 +174,9 @@ int scratch_alloc(void** p, size_t bytes, cudaStream_t st) {
   if (bytes == 0) return FAVOR_OK;
   cudaMemPool_t pool = pool_for_device();
   if (!pool) return FAVOR_ERR_CUDA;
-  return cudaMallocFromPoolAsync(p, bytes, pool, st) == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA;
+  if (cudaMallocFromPoolAsync(p, bytes, pool, st) == cudaSuccess) return FAVOR_OK;
+  cudaGetLastError();  // the refusal is this call's alone: the next launch must not report it
+  return FAVOR_ERR_CUDA;
 }
 
 // Two non-blocking streams per device for the host-buffer entry's copies in and out, created on

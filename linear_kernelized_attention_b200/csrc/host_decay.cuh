@@ -69,11 +69,12 @@ size_t decay_cc_workspace(int B, int H, int L, int d, int nstates) {
 }
 
 // A launch that may start while the kernel before it in the stream drains (the kernel waits for that
-// one's results itself) where `pdl` is set.
+// one's results itself) where `pdl` is set. Its own status alone is looked at: an error that an earlier call of the
+// process left behind is not this call's, and one of this call is not left for the next.
 template <typename P>
-int launch_with(void (*kern)(P), long long grid, int threads, int smem, cudaStream_t st, bool pdl, const P& p) {
+int launch_with(void (*kern)(P), dim3 grid, int threads, int smem, cudaStream_t st, bool pdl, const P& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -82,7 +83,9 @@ int launch_with(void (*kern)(P), long long grid, int threads, int smem, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess) return FAVOR_OK;
+  cudaGetLastError();
+  return FAVOR_ERR_CUDA;
 }
 
 // The scan over `nseg` segments of `seg` tokens whose updates lie in ws.
@@ -349,11 +352,8 @@ int launch_decay_step(const dcy::StepParams& p0, int BH, int d, cudaStream_t st)
   p.slices = (d + p.cols - 1) / p.cols;
   if ((long long)BH * p.slices > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)((long long)BH * p.slices);
-  if (vec)
-    dcy::k_decay_step<T, 4, 8><<<grid, dcy::kStepThreads, 0, st>>>(p);
-  else
-    dcy::k_decay_step<T, 1, 8><<<grid, dcy::kStepThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA;
+  return launch_with<dcy::StepParams>(vec ? dcy::k_decay_step<T, 4, 8> : dcy::k_decay_step<T, 1, 8>, grid,
+                                      dcy::kStepThreads, 0, st, false, p);
 }
 
 template <typename T, int V, bool INTER>
@@ -370,8 +370,8 @@ int launch_rotary_t(favor::rot::Params p, cudaStream_t st) {
   p.groups = (heads + p.per_group - 1) / p.per_group;
   const unsigned gx = (unsigned)std::min<long long>(blocks, 64ll * sms);
   if (p.groups > 65535) return FAVOR_ERR_UNSUPPORTED;
-  favor::rot::k_rotary<T, V, INTER><<<dim3(gx, p.groups), favor::rot::kThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA;
+  return launch_with<favor::rot::Params>(favor::rot::k_rotary<T, V, INTER>, dim3(gx, p.groups), favor::rot::kThreads, 0,
+                                         st, false, p);
 }
 
 template <typename T>

@@ -200,3 +200,24 @@ def test_stream_handle_of_the_default_stream():
     S, ref = torch.zeros(2, 2, 4, 64, 64, device="cuda")
     want = F.favor_decay_step(q, k, v, g, ref)
     assert torch.equal(F.favor_decay_step(q, k, v, g, S, stream=0), want) and torch.equal(S, ref)
+
+
+def test_a_call_refused_for_scratch_leaves_no_error_behind():
+    """2^22 heads of one token at d = 128 want 64 KB of chunk states each, 275 GB: refused before any launch. The
+    next calls, here a token step that updates its state in place, must not report it."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    B, d = 2 ** 22, 128
+    assert F.favor_decay_workspace_bytes(B, 1, 1, d, 0) > torch.cuda.get_device_properties(0).total_memory
+    x = torch.zeros(1, 1, 1, d, device="cuda").expand(B, 1, 1, d)
+    out = torch.empty(B, 1, 1, d, device="cuda")
+    g = torch.full((1,), -0.1, device="cuda")
+    with pytest.raises(F.FavorError) as e:
+        F.favor_decay_attention(x, x, x, g, out=out)
+    assert e.value.code == -6
+    q = torch.randn(2, 1, 64, device="cuda")
+    S = torch.zeros(2, 1, 64, 64, device="cuda")
+    row = F.favor_decay_step(q, q, q, g, S)
+    freq, _ = F.favor_rotary_frequencies(64, device="cuda")
+    F.favor_rotary(q[:, :, None], None, freq)
+    assert torch.allclose(row, q * (q * q).sum(-1, keepdim=True), rtol=1e-5) and F.favor_sync_status() == 0
