@@ -553,7 +553,7 @@ def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
         with on:
             return favor_decay_step(q, k, v, log_decay, state, out)
     shape, dt = q.shape, q.dtype
-    B, H, d = shape
+    B, H, d = _dims(shape)
     if log_decay is None or state is None:
         raise TypeError("log_decay and state must be float32 tensors")
     g = _aux("log_decay", log_decay, (H,), torch.float32, dev)
@@ -569,6 +569,8 @@ def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
 
 
 def favor_decay_workspace_bytes(B, H, L, d, dtype_code=1, backward=False) -> int:
+    if max(B, H, L, d) > 0x7fffffff:
+        return 0  # not a size the calls take
     return lib().favor_decay_workspace_bytes(B, H, L, d, int(dtype_code), int(backward))
 
 
@@ -578,6 +580,7 @@ def favor_rotary_frequencies(rot, base=10000.0, scaling=FAVOR_ROTARY_PLAIN, fact
     """(freq, rot_scale): float64 [rot/2] radians per position, on `device` (CPU if None), and the scale of
     the rotated columns to pass to favor_rotary. Scalings: favor_rotary_frequencies in include/favor.h."""
     import torch
+    _dims((rot,))
     freq = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
     rs = ctypes.c_double(1.0)
     rc = lib().favor_rotary_frequencies(freq.data_ptr(), ctypes.addressof(rs), int(rot), float(base), int(scaling),
@@ -607,7 +610,7 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise TypeError("k must be a CUDA tensor of shape [B, Hk, L, d]")
-        Hk = k.shape[1]
+        Hk = _dims(k.shape)[1]
         if k_out is None:
             k_out = _new(k, False)
         (pk, pko), wk = _operands((B, Hk, L, d), dt, dev, ("k", "k_out"), k, k_out)
@@ -617,12 +620,13 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
         raise ValueError("first_position must fit 32 bits")
     if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
         raise TypeError("freq must be a float64 tensor of shape [rot/2]")
+    (rot,) = _dims((2 * freq.shape[0],))
     f = _aux("freq", freq, freq.shape, torch.float64, dev)
     pos = _aux("positions", positions, (B, L), torch.int32, dev)
     if q_out is None:
         q_out = _new(q, False)
     (pq, pqo), wq = _operands(shape, dt, dev, ("q", "q_out"), q, q_out)
-    rc = lib().favor_rotary(pq, pk, f, pos, pqo, pko, B, Hq, Hk, L, d, 2 * freq.shape[0], int(interleaved), int(inverse),
+    rc = lib().favor_rotary(pq, pk, f, pos, pqo, pko, B, Hq, Hk, L, d, rot, int(interleaved), int(inverse),
                             int(first_position), scale, rot_scale, code,
                             None if wq and wk else _strides(q, k, q_out, k_out), _handle(dev))
     if rc != 0:

@@ -146,3 +146,26 @@ def test_stream_handle_zero_is_the_default_stream(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
     assert F._elsewhere(dev, 0).of == "default"
     assert F._elsewhere(dev, 64).of == 64
+
+
+def test_every_entry_refuses_sizes_past_int(monkeypatch):
+    """The C layer takes int: 2^32 + 5 would arrive as 5, and most of the batch would be left out without a word.
+    Expanded tensors without storage stand in for the operands; the checks before the sizes are let through."""
+    import torch
+    monkeypatch.setattr(F, "_first", lambda name, t, dims: 1)
+    monkeypatch.setattr(F, "_elsewhere", lambda device, stream: None)
+    big, none = 2 ** 32 + 5, torch.empty(1, device="meta")
+    x = torch.empty(1, 1, 8, device="meta", dtype=torch.bfloat16)
+    for shape in ((big, 1, 8), (1, big, 8)):
+        t = x.expand(shape)
+        with pytest.raises(ValueError, match="exceeds 2"):
+            F.favor_decay_step(t, t, t, none, none)
+    q = x[:, :, None]
+    for shape in ((1, big, 1, 8), (big, 1, 1, 8)):
+        with pytest.raises(ValueError, match="exceeds 2"):
+            F.favor_rotary(q, q.expand(shape), torch.empty(4, device="meta", dtype=torch.float64))
+    with pytest.raises(ValueError, match="exceeds 2"):
+        F.favor_rotary(q, None, torch.empty(2 ** 31 + 4, device="meta", dtype=torch.float64))
+    with pytest.raises(ValueError, match="exceeds 2"):
+        F.favor_rotary_frequencies(2 ** 32 + 8)
+    assert F.favor_decay_workspace_bytes(1, 1, big, 64) == 0 == F.favor_decay_workspace_bytes(big, 1, 8, 64, 0)
