@@ -66,7 +66,7 @@ typedef enum {
 typedef enum {
   FAVOR_OK = 0,
   FAVOR_ERR_NULL = -1,        /* a required pointer is NULL */
-  FAVOR_ERR_ALIGN = -2,       /* a pointer is not 16-byte aligned */
+  FAVOR_ERR_ALIGN = -2,       /* a pointer is not 16-byte aligned, or not as its entry asks */
   FAVOR_ERR_SHAPE = -3,       /* a size is non-positive or the total overflows */
   FAVOR_ERR_KIND = -4,        /* feature_kind is not FAVOR_TRIG / FAVOR_RELU */
   FAVOR_ERR_UNSUPPORTED = -5, /* a valid shape the library has no kernel for */
@@ -279,8 +279,10 @@ int favor_decode_step(const void* q, const void* k, const void* v, const void* o
  *   strides: NULL (contiguous), or one favor_strides per operand in argument order, so that
  *   token-major projections and slices of fused ones are read in place. d is contiguous. Inputs
  *   may have stride 0 (a broadcast head); an output whose rows overlap returns FAVOR_ERR_SHAPE.
- *   Base pointers are 16-byte aligned. Outputs must not overlap inputs; an output pointer equal to
- *   an input's returns FAVOR_ERR_UNSUPPORTED.
+ *   Base pointers: 16-byte aligned where d and every stride of the operand are whole 16-byte pieces
+ *   (multiples of 8 bf16 or 4 floats; steps of dimensions of one do not count), aligned to their
+ *   element otherwise, so that slices of such rows start anywhere; else FAVOR_ERR_ALIGN. Outputs must
+ *   not overlap inputs; an output pointer equal to an input's returns FAVOR_ERR_UNSUPPORTED.
  * log_decay: device float [H], 4-byte aligned, natural logarithm of the decay: <= 0, -infinity
  *   (lambda = 0: each token by itself) included. A positive value grows the state instead, and is
  *   used as it is as long as exp(128 log_decay) is finite.
@@ -343,8 +345,8 @@ size_t favor_decay_workspace_bytes(int B, int H, int L, int d, int dtype_code, i
  * freq: device double [rot/2], radians per position (favor_rotary_frequencies). positions: device int
  * [B, L], or NULL for first_position + t. Angles are reduced in double, so far positions keep their
  * accuracy. k, k_out: NULL with Hk = 0. q_out may be q and k_out may be k with the same strides (in
- * place). strides: q, k, q_out, k_out (NULL = contiguous). Data pointers are 16-byte aligned, freq
- * 8-byte, positions 4-byte. Supported: rot even, 2 <= rot <= d <= 65536, Hq + Hk <= 65535.
+ * place). strides: q, k, q_out, k_out (NULL = contiguous). Data pointers are aligned as
+ * favor_decay_attention's, freq to 8 bytes, positions to 4. Supported: rot even, 2 <= rot <= d <= 65536, Hq + Hk <= 65535.
  */
 int favor_rotary(const void* q, const void* k, const double* freq, const int* positions, void* q_out,
                  void* k_out, int B, int Hq, int Hk, int L, int d, int rot, int interleaved, int inverse,

@@ -473,7 +473,7 @@ def favor_decay_attention(q, k, v, log_decay, state=None, lengths=None, out=None
                           return_state=False, stream=None):
     """Causal linear attention with a decay per head: S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
     out_t = S_t^T q_t (favor_decay_attention in include/favor.h). q, k, v: [B, H, L, d] bf16 or float32,
-    any strides with d contiguous; log_decay: float32 [H]; state: float32 [B, H, d, d] carried in, or
+    any strides with d contiguous (a tensor whose rows are whole 16-byte pieces starts on one); log_decay: float32 [H]; state: float32 [B, H, d, d] carried in, or
     None; lengths: int32 [B] or None. Returns out, or (out, state_out) where return_state is true or
     state_out is given. Rows past a sequence's length are left as they were in a given `out`, and zero
     in a new one. state_out may be `state`."""
@@ -543,8 +543,8 @@ def favor_decay_attention_backward(q, k, v, log_decay, dout, state=None, dstate=
 
 def favor_decay_step(q, k, v, log_decay, state, out=None, stream=None):
     """One token per head against the carried state, updated in place: S = exp(log_decay[h]) S + k v^T,
-    out = S^T q. q, k, v: [B, H, d] bf16 or float32 (slices of fused projections are read in place);
-    state: float32 [B, H, d, d]. Returns out [B, H, d]."""
+    out = S^T q. q, k, v: [B, H, d] bf16 or float32 (slices of fused projections are read in place, strides and
+    alignment as for favor_decay_attention); state: float32 [B, H, d, d]. Returns out [B, H, d]."""
     import torch
     code = _first("q", q, 3)
     dev = q.device
@@ -593,7 +593,7 @@ def favor_rotary(q, k, freq, positions=None, first_position=0, interleaved=False
                  rot_scale=1.0, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [B, Hq, L, d] and k [B, Hk, L, d] (or None) in one launch: the first
     2 len(freq) columns turn by positions * freq, all are multiplied by `scale`, the rotated ones by
-    rot_scale too. freq: float64 [rot/2]; positions: int32 [B, L], or None for first_position + t.
+    rot_scale too. Strides and alignment as for favor_decay_attention. freq: float64 [rot/2]; positions: int32 [B, L], or None for first_position + t.
     inverse=True is the gradient of the same call. q_out / k_out may be q / k (in place). Returns
     (q_out, k_out)."""
     import torch

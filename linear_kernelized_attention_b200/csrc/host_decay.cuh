@@ -38,6 +38,14 @@ int make_view(View* v, const void* p, const favor_strides* s, int i, int B, int 
   return last < (double)lim ? FAVOR_OK : FAVOR_ERR_SHAPE;
 }
 
+// Where an operand's rows are whole 16-byte pieces they are moved as such, and its base must lie on one; other rows
+// are read element by element, and slices of them start anywhere.
+bool view_aligned(const View& v, int d, int dtype_code) {
+  const int es = dtype_code == 1 ? 2 : 4, n = 16 / es;
+  const bool pieces = d % n == 0 && v.sb % n == 0 && v.sh % n == 0 && v.st % n == 0;
+  return (reinterpret_cast<uintptr_t>(v.p) & (pieces ? 15u : es - 1u)) == 0;
+}
+
 // An output's rows must not overlap one another: in order of stride, each dimension steps past
 // everything the smaller ones span.
 bool rows_distinct(const View& v, int B, int H, int L, int d) {
@@ -400,7 +408,7 @@ int favor_decay_attention(const void* q, const void* k, const void* v, const flo
                           const int* lengths, void* out, float* state_out, int B, int H, int L, int d,
                           int dtype_code, const favor_strides* strides, void* stream) {
   if (!q || !k || !v || !log_decay || !out) return FAVOR_ERR_NULL;
-  if (bad_align({q, k, v, out, state_in, state_out}) || ((uintptr_t)log_decay & 3) || ((uintptr_t)lengths & 3))
+  if (bad_align({state_in, state_out}) || ((uintptr_t)log_decay & 3) || ((uintptr_t)lengths & 3))
     return FAVOR_ERR_ALIGN;
   int rc = check_decay_sizes(B, H, L, d, dtype_code);
   if (rc != FAVOR_OK) return rc;
@@ -411,6 +419,8 @@ int favor_decay_attention(const void* q, const void* k, const void* v, const flo
       (rc = make_view(&vv, v, strides, 2, B, H, L, d)) != FAVOR_OK ||
       (rc = make_view(&vo, out, strides, 3, B, H, L, d)) != FAVOR_OK)
     return rc;
+  for (const View* x : {&vq, &vk, &vv, &vo})
+    if (!view_aligned(*x, d, dtype_code)) return FAVOR_ERR_ALIGN;
   if (!rows_distinct(vo, B, H, L, d)) return FAVOR_ERR_SHAPE;
   if (out == q || out == k || out == v) return FAVOR_ERR_UNSUPPORTED;
   if ((rc = check_device()) != FAVOR_OK) return rc;
@@ -428,8 +438,7 @@ int favor_decay_attention_backward(const void* q, const void* k, const void* v, 
                                    const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in, int B,
                                    int H, int L, int d, int dtype_code, const favor_strides* strides, void* stream) {
   if (!q || !k || !v || !log_decay || !dout || !dq || !dk || !dv) return FAVOR_ERR_NULL;
-  if (bad_align({q, k, v, dout, dq, dk, dv, state_in, dstate_out, dstate_in}) || ((uintptr_t)log_decay & 3) ||
-      ((uintptr_t)lengths & 3))
+  if (bad_align({state_in, dstate_out, dstate_in}) || ((uintptr_t)log_decay & 3) || ((uintptr_t)lengths & 3))
     return FAVOR_ERR_ALIGN;
   int rc = check_decay_sizes(B, H, L, d, dtype_code);
   if (rc != FAVOR_OK) return rc;
@@ -437,6 +446,8 @@ int favor_decay_attention_backward(const void* q, const void* k, const void* v, 
   const void* ptr[7] = {q, k, v, dout, dq, dk, dv};
   for (int i = 0; i < 7; ++i)
     if ((rc = make_view(&x[i], ptr[i], strides, i, B, H, L, d)) != FAVOR_OK) return rc;
+  for (const View& v : x)
+    if (!view_aligned(v, d, dtype_code)) return FAVOR_ERR_ALIGN;
   for (int i = 4; i < 7; ++i) {
     if (!rows_distinct(x[i], B, H, L, d)) return FAVOR_ERR_SHAPE;
     for (int j = 0; j < i; ++j)
@@ -462,7 +473,7 @@ int favor_decay_attention_backward(const void* q, const void* k, const void* v, 
 int favor_decay_step(const void* q, const void* k, const void* v, const float* log_decay, float* state, void* out,
                      int B, int H, int d, int dtype_code, const favor_strides* strides, void* stream) {
   if (!q || !k || !v || !log_decay || !state || !out) return FAVOR_ERR_NULL;
-  if (bad_align({q, k, v, out, state}) || ((uintptr_t)log_decay & 3)) return FAVOR_ERR_ALIGN;
+  if (bad_align({state}) || ((uintptr_t)log_decay & 3)) return FAVOR_ERR_ALIGN;
   int rc = check_decay_sizes(B, H, 1, d, dtype_code);
   if (rc != FAVOR_OK) return rc;
   dcy::StepParams p{};
@@ -471,6 +482,8 @@ int favor_decay_step(const void* q, const void* k, const void* v, const float* l
       (rc = make_view(&p.v, v, strides, 2, B, H, 1, d)) != FAVOR_OK ||
       (rc = make_view(&p.y, out, strides, 3, B, H, 1, d)) != FAVOR_OK)
     return rc;
+  for (const View* x : {&p.q, &p.k, &p.v, &p.y})
+    if (!view_aligned(*x, d, dtype_code)) return FAVOR_ERR_ALIGN;
   if (!rows_distinct(p.y, B, H, 1, d)) return FAVOR_ERR_SHAPE;
   if (out == q || out == k || out == v) return FAVOR_ERR_UNSUPPORTED;
   if ((rc = check_device()) != FAVOR_OK) return rc;
@@ -487,8 +500,7 @@ int favor_rotary(const void* q, const void* k, const double* freq, const int* po
                  float scale, float rot_scale, int dtype_code, const favor_strides* strides, void* stream) {
   if (!q || !freq || !q_out || (Hk > 0 && (!k || !k_out))) return FAVOR_ERR_NULL;
   if (Hk < 0) return FAVOR_ERR_SHAPE;
-  if (bad_align({q, q_out}) || (Hk > 0 && bad_align({k, k_out})) || ((uintptr_t)freq & 7) || ((uintptr_t)positions & 3))
-    return FAVOR_ERR_ALIGN;
+  if (((uintptr_t)freq & 7) || ((uintptr_t)positions & 3)) return FAVOR_ERR_ALIGN;
   if (B <= 0 || Hq <= 0 || L <= 0 || d <= 0 || rot <= 0 || rot % 2 != 0 || rot > d) return FAVOR_ERR_SHAPE;
   const long long heads = (long long)Hq + Hk;
   if ((double)B * heads * L * d > (double)(1ll << 40)) return FAVOR_ERR_SHAPE;
@@ -501,6 +513,8 @@ int favor_rotary(const void* q, const void* k, const double* freq, const int* po
   if (Hk > 0 && ((rc = make_view(&p.k, k, strides, 1, B, Hk, L, d)) != FAVOR_OK ||
                  (rc = make_view(&p.ky, k_out, strides, 3, B, Hk, L, d)) != FAVOR_OK))
     return rc;
+  for (const View* x : {&p.q, &p.k, &p.qy, &p.ky})  // views that are not there are null
+    if (!view_aligned(*x, d, dtype_code)) return FAVOR_ERR_ALIGN;
   if (!rows_distinct(p.qy, B, Hq, L, d) || (Hk > 0 && !rows_distinct(p.ky, B, Hk, L, d))) return FAVOR_ERR_SHAPE;
   auto same = [](const View& a, const View& b) { return a.sb == b.sb && a.sh == b.sh && a.st == b.st; };
   // in place means the very same rows; q's output over k (or k's over q) has no order

@@ -169,3 +169,27 @@ def test_every_entry_refuses_sizes_past_int(monkeypatch):
     with pytest.raises(ValueError, match="exceeds 2"):
         F.favor_rotary_frequencies(2 ** 32 + 8)
     assert F.favor_decay_workspace_bytes(1, 1, big, 64) == 0 == F.favor_decay_workspace_bytes(big, 1, 8, 64, 0)
+
+
+# operands that are not whole 16-byte pieces need their element's alignment alone: the call gets as far as the
+# output that is an input (-5), which the host refuses before any CUDA call
+@pytest.mark.parametrize("dt,off,d,st,code", [
+    (1, 2, 20, None, -5), (1, 8, 33, None, -5), (1, 1, 20, None, -2), (0, 4, 33, None, -5), (0, 2, 33, None, -2),
+    (1, 2, 64, None, -2), (0, 4, 64, None, -2),                           # whole pieces: as before
+    (1, 2, 64, (1028, 512, 64), -5), (0, 4, 64, (1026, 512, 64), -5),    # rows of whole pieces, odd strides
+])
+def test_alignment_follows_the_rows(dt, off, d, st, code):
+    o = dict(q=4096 + off, k=8192 + off, v=12288 + off, out=4096 + off, d=d, dt=dt)
+    n = lambda i: None if st is None else _strides([st] * i)
+    assert _attend(**o, st=n(4)) == code
+    assert _step(**o, st=n(4)) == code
+    g = dict(q=4096 + off, k=8192 + off, v=12288 + off, do=16384 + off, dq=4096 + off, dk=20480 + off, dv=24576 + off)
+    assert _backward(**g, d=d, dt=dt, st=n(7)) == code
+    r = dict(q=4096 + off, k=8192 + off, qo=12288 + off, ko=4096 + off, d=d, rot=16, dt=dt)
+    assert _rotary(**r, st=n(4)) == code
+
+
+def test_states_stay_on_16_bytes():
+    assert _attend(d=20, s_in=20) == -2 and _attend(d=33, s_out=40) == -2
+    assert _step(d=33, s=84) == -2
+    assert _backward(d=20, ds=4) == -2 and _backward(d=20, ds_in=24) == -2

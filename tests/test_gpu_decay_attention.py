@@ -481,3 +481,67 @@ def test_refusals():
     assert e.value.code == -5
     torch.cuda.synchronize()
     assert F.favor_sync_status() == 0
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("H,d", [(2, 20), (2, 33), (1, 20), (3, 100)])
+def test_slices_of_rows_that_are_not_whole_pieces(H, d, name):
+    """Token slices, split prompts and fused projections of odd heads start anywhere: the same results as their
+    copies, bit for bit."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    x = torch.randn(2, 90, 3, H, d, device="cuda").to(_dtype(name)) * 0.5  # fused [B, L, 3, H, d]
+    do = torch.randn(2, H, 90, d, device="cuda").to(_dtype(name))
+    g = torch.from_numpy(C.slopes(H)).cuda()
+    q, k, v = (x[:, :, i].transpose(1, 2) for i in range(3))
+    c = [t.contiguous() for t in (q, k, v)]
+    if d * x.element_size() % 16:
+        assert any(t.data_ptr() % 16 for t in (q, k, v, x[:, 1:], do[:, :, 41:]))
+    ref = F.favor_decay_attention(*c, g, return_state=True)
+    got = F.favor_decay_attention(q, k, v, g, return_state=True)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    for a, b in zip(F.favor_decay_attention_backward(q, k, v, g, do), F.favor_decay_attention_backward(*c, g, do)):
+        assert torch.equal(a, b)
+    # the prompt in two parts, outputs and gradients into slices too
+    cut = lambda t, a, b: t[:, :, a:b]
+    S1, S2 = torch.zeros(2, 2, H, d, d, device="cuda")
+    out = torch.empty_like(c[0])
+    dq, dk, dv = (torch.empty_like(t) for t in c)
+    for a, b in ((0, 41), (41, 90)):
+        part, whole = [cut(t, a, b) for t in c], [cut(t, a, b).contiguous() for t in c]
+        F.favor_decay_attention(*part, g, state=S1, out=cut(out, a, b), state_out=S1)
+        ref, _ = F.favor_decay_attention(*whole, g, state=S2, state_out=S2)
+        assert torch.equal(cut(out, a, b), ref) and torch.equal(S1, S2)
+        F.favor_decay_attention_backward(*part, g, cut(do, a, b), dq=cut(dq, a, b), dk=cut(dk, a, b), dv=cut(dv, a, b))
+        for t, w in zip((dq, dk, dv), F.favor_decay_attention_backward(*whole, g, cut(do, a, b).contiguous())):
+            assert torch.equal(cut(t, a, b), w)
+    # single tokens of the contiguous prompt
+    S1, S2 = torch.zeros(2, 2, H, d, d, device="cuda")
+    for t in range(9):
+        row = F.favor_decay_step(*(y[:, :, t] for y in c), g, S1, out=out[:, :, t])
+        assert torch.equal(row, F.favor_decay_step(*(y[:, :, t].contiguous() for y in c), g, S2))
+    assert torch.equal(S1, S2)
+    freq, _ = F.favor_rotary_frequencies(d // 2 * 2, device="cuda")
+    for a, b in zip(F.favor_rotary(q[:, :, 3:], k[:, :, 3:], freq),
+                    F.favor_rotary(q[:, :, 3:].contiguous(), k[:, :, 3:].contiguous(), freq)):
+        assert torch.equal(a, b)
+    assert F.favor_sync_status() == 0
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_rows_of_whole_pieces_between_odd_strides(name):
+    """d = 64 in rows of 67 elements, from an odd element on."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    wide = [torch.randn(2, 3, 150, 67, device="cuda").to(_dtype(name)) for _ in range(4)]
+    q, k, v, do = (t[..., 1:65] for t in wide)
+    g = torch.from_numpy(C.slopes(3)).cuda()
+    c = [t.contiguous() for t in (q, k, v, do)]
+    # the copies of bf16 rows go to the tensor cores, these to the CUDA cores: within twice the norms that
+    # decay_cases.check allows each, 2 x 2 sqrt(2 / 3) 2^-8 < 2^-6 and 2 x 2^-19
+    (r, rS), (o, S) = (F.favor_decay_attention(*t[:3], g, return_state=True) for t in (c, (q, k, v)))
+    tol = 2.0 ** -6 if name == "bf16" else 0.0
+    assert float((o.float() - r.float()).norm()) <= tol * float(r.float().norm())
+    assert float((S - rS).norm()) <= (2.0 ** -18 if name == "bf16" else 0.0) * float(rS.norm())
+    for a, b in zip(F.favor_decay_attention_backward(q, k, v, g, do), F.favor_decay_attention_backward(*c[:3], g, c[3])):
+        assert float((a.float() - b.float()).norm()) <= tol * float(b.float().norm())
