@@ -295,7 +295,8 @@ int favor_decode_step(const void* q, const void* k, const void* v, const void* o
  * run on the tensor cores: fp32 accumulation, the weighted scores and the carried state rounded to bf16
  * on their way into `out`; everything else on CUDA cores in fp32. States are returned to fp32 accuracy either way.
  * Infinities and NaN reach what the recurrence takes them to, and nothing before them (an infinity on its way
- * through a state may come out as NaN; on the tensor cores a chunk of 128 tokens that holds one takes longer).
+ * through a state may come out as NaN; on the tensor cores the first chunk of 128 tokens that holds one takes up to
+ * 0.9 ms longer at d <= 64 and 3.3 ms above, later ones about as long as any).
  */
 typedef struct {
   int64_t batch, head, token; /* element strides of a [B, H, L, d] operand */
