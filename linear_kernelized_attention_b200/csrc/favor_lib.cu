@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "../../include/favor.h"
+#include "smem_table.h"
 #include "ptx.cuh"
 #include "kernels_f32.cuh"
 #include "kernel_bidir_split.cuh"
@@ -81,21 +82,15 @@ int sm_count() {
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (kernel, device): the attribute
 // persists, and setting it on every call costs host time on the launch path.
 int ensure_smem_attr(const void* kern, int bytes) {
-  struct Entry {
-    const void* k;
-    int dev, bytes;
-  };
-  static Entry done[64];
-  static int n = 0;
+  static SmemTable done;
   static std::mutex mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FAVOR_ERR_CUDA;
   std::lock_guard<std::mutex> g(mu);
-  for (int i = 0; i < n; ++i)
-    if (done[i].k == kern && done[i].dev == dev && done[i].bytes >= bytes) return FAVOR_OK;
+  if (done.known(kern, dev, bytes)) return FAVOR_OK;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return FAVOR_ERR_CUDA;
-  if (n < 64) done[n++] = Entry{kern, dev, bytes};
+  done.set(kern, dev, bytes);
   return FAVOR_OK;
 }
 
