@@ -98,3 +98,41 @@ def rotary_allowed(ref, x, h, interleaved, scale, rot_scale, bf16):
     (6 x 2^-24 of the pair with the sum's); then one rounding of the result to its type."""
     mag = pair_mag(x, h, interleaved, scale, rot_scale)
     return (6 * U32 + 2.0 ** -22) * mag + (UBF if bf16 else U32) * np.abs(ref) * (1 + 2.0 ** -7) + 1e-37
+
+
+def scan64(a, b, c, g, X=None, reverse=False, block=256):
+    """The scan job of all four outputs in 64 bits, a block of tokens at a time (the oracle's recurrence takes one token
+    at a time, too slow for long sequences; it pins this one): y_i = sum over j <= i (reverse: j >= i) of lambda^|i-j|
+    (a_i . b_j) c_j + lambda^(distance to X) a_i X, and the X handed on. Torch tensors [B, H, L, d] on any device."""
+    import torch
+    a, b, c = (x.double().flip(2) if reverse else x.double() for x in (a, b, c))
+    B, H, L, d = a.shape
+    g = torch.as_tensor(np.asarray(g), dtype=torch.float64, device=a.device)[:, None]
+    e0 = 0 if reverse else 1  # X is handed over before (reverse: after) the decay of the step it crosses
+    pw = lambda n: torch.where(n == 0, torch.ones_like(g * n), torch.exp(g * n))
+    X = torch.zeros(B, H, d, c.shape[-1], dtype=torch.float64, device=a.device) if X is None else X.double().clone()
+    y = torch.empty(B, H, L, c.shape[-1], dtype=torch.float64, device=a.device)
+    for t in range(0, L, block):
+        n = min(block, L - t)
+        r = torch.arange(n, device=a.device, dtype=torch.float64)
+        x, z, w = a[:, :, t:t + n], b[:, :, t:t + n], c[:, :, t:t + n]
+        gap = r[:, None] - r[None, :]
+        D = torch.where(gap >= 0, pw(gap.clamp(min=0).reshape(-1)).reshape(H, n, n), torch.zeros((), dtype=torch.float64,
+                                                                                                 device=a.device))
+        y[:, :, t:t + n] = ((x @ z.transpose(-1, -2)) * D) @ w + pw(r + e0)[..., None] * (x @ X)
+        X = pw(torch.full((1,), float(n), device=a.device, dtype=torch.float64))[..., None] * X \
+            + (pw(n - r - e0)[..., None] * z).transpose(-1, -2) @ w
+    return (y.flip(2) if reverse else y), X
+
+
+def forward64(q, k, v, g, S=None):
+    return scan64(q, k, v, g, S)
+
+
+def backward64(q, k, v, g, do, S=None, dS=None):
+    """(dq, dk, dv, dstate_in)."""
+    T = lambda x: None if x is None else x.transpose(-1, -2)
+    dq, _ = scan64(do, v, k, g, T(S))
+    dk, _ = scan64(v, do, q, g, T(dS), reverse=True)
+    dv, G = scan64(k, q, do, g, dS, reverse=True)
+    return dq, dk, dv, G

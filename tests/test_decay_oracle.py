@@ -129,3 +129,21 @@ def test_rotary_frequencies_refuse(args, kw, code):
     with pytest.raises(F.FavorError) as e:
         F.favor_rotary_frequencies(*args, **kw)
     assert e.value.code == code
+
+
+@pytest.mark.parametrize("block", [1, 7, 16, 64])
+def test_blocked_reference_equals_recurrence(block, monkeypatch):
+    """The 64-bit reference of the long tests, against the recurrence: forward, gradients, states, every kind of decay."""
+    import torch
+
+    import decay_cases as C
+    monkeypatch.setattr(C.scan64, "__defaults__", (None, False, block))
+    g = np.array([-0.3, 0.0, -np.inf, -40.0])
+    q, k, v, do = _inputs(2, 4, 33, 5, 11)
+    S, dS = np.random.default_rng(12).standard_normal((2, 2, 4, 5, 5))
+    t = [torch.from_numpy(x) for x in (q, k, v, do, S, dS)]
+    got = [*C.forward64(*t[:3], g, t[4]), *C.backward64(*t[:3], g, t[3], t[4], t[5])]
+    want = [*D.decay_attention(q, k, v, g, S), *D.decay_backward(q, k, v, g, do, S, dS)]
+    for a, b in zip(got, want):
+        assert np.allclose(a.numpy(), b, atol=1e-11)
+    assert np.allclose(C.forward64(*t[:3], g)[0].numpy(), D.decay_attention(q, k, v, g)[0], atol=1e-11)
