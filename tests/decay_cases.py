@@ -136,3 +136,20 @@ def backward64(q, k, v, g, do, S=None, dS=None):
     dk, _ = scan64(v, do, q, g, T(dS), reverse=True)
     dv, G = scan64(k, q, do, g, dS, reverse=True)
     return dq, dk, dv, G
+
+
+def coarse_slope():
+    """A log decay whose exp lies far from the fp32 values beside it: rounding it is off by a quarter of a step at least."""
+    g = np.float32(-1e-3) - np.arange(200, dtype=np.float32) * np.float32(1e-6)
+    lam = np.exp(g.astype(np.float64))
+    off = np.abs(lam.astype(np.float32).astype(np.float64) / lam - 1)
+    i = int(off.argmax())
+    assert off[i] >= 2.0 ** -26
+    return float(g[i])
+
+
+def drift_allowed(steps):
+    """The mean signed relative error of decaying elements, over many of them: each step rounds each once, by at most
+    2^-24 and to either side, so one element has a standard deviation of sqrt(steps / 3) 2^-24 and the mean of N a
+    sqrt(N)-th of it. A decay rounded to fp32 moves all elements to one side, steps times."""
+    return np.sqrt(steps) * U32

@@ -147,3 +147,20 @@ def test_blocked_reference_equals_recurrence(block, monkeypatch):
     for a, b in zip(got, want):
         assert np.allclose(a.numpy(), b, atol=1e-11)
     assert np.allclose(C.forward64(*t[:3], g)[0].numpy(), D.decay_attention(q, k, v, g)[0], atol=1e-11)
+
+
+def test_drift_bound_tells_a_rounded_decay_from_an_exact_one():
+    """4096 steps of a decaying state in fp32 on the CPU: with lambda as one fp32 value the mean error is past the
+    bound, with its remainder carried well inside it."""
+    import decay_cases as C
+    T, g = 4096, C.coarse_slope()
+    lam = math.exp(g)
+    lh = np.float32(lam)
+    ll = np.float32(lam - float(lh))
+    s0 = np.random.default_rng(3).standard_normal(4096).astype(np.float32)
+    one, two = s0.copy(), s0.copy()
+    for _ in range(T):
+        one = one * lh
+        two = (two.astype(np.float64) * lh + (two * ll).astype(np.float64)).astype(np.float32)  # a fused update
+    mean = lambda s: abs(np.mean(s.astype(np.float64) / (s0.astype(np.float64) * lam ** T) - 1))
+    assert mean(two) <= 0.1 * C.drift_allowed(T) and mean(one) >= 5 * C.drift_allowed(T)

@@ -221,3 +221,27 @@ def test_a_call_refused_for_scratch_leaves_no_error_behind():
     freq, _ = F.favor_rotary_frequencies(64, device="cuda")
     F.favor_rotary(q[:, :, None], None, freq)
     assert torch.allclose(row, q * (q * q).sum(-1, keepdim=True), rtol=1e-5) and F.favor_sync_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 33])
+def test_step_decay_does_not_drift(d):
+    """4096 tokens with k = 0: the state is lambda^4096 of the first one's. lambda rounded to fp32 would shift every
+    element to one side by 4096 roundings (the CPU test beside the oracle shows it past the bound)."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    T, g = 4096, C.coarse_slope()
+    S, Sn = C.draw((2, 2, d, d), 5, torch.float32)
+    S, gg = S.cuda(), torch.tensor([g, g], device="cuda")
+    q, v = (torch.randn(2, 2, d, device="cuda") for _ in range(2))
+    k, out = torch.zeros_like(q), torch.empty_like(q)
+    F.favor_decay_step(q, k, v, gg, torch.zeros_like(S), out=out)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        for _ in range(64):
+            F.favor_decay_step(q, k, v, gg, S, out=out)
+    for _ in range(T // 64):
+        gr.replay()
+    rel = S.double().cpu().numpy() / (Sn * np.exp(g * T)) - 1
+    assert abs(rel.mean()) <= C.drift_allowed(T)
+    assert np.abs(rel).max() <= T * C.U32
