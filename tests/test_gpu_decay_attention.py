@@ -617,3 +617,16 @@ def test_a_call_on_nan_takes_about_as_long_as_any_other(d, names):
     clean = us(x)
     bad = us({n: torch.full_like(t, float("nan")) if n in names else t for n, t in x.items()})
     assert bad <= 10 * clean, (clean, bad)
+
+
+@pytest.mark.parametrize("name,d", [("bf16", 64), ("bf16", 128), ("bf16", 20), ("f32", 64)])
+def test_broadcast_head_is_its_copies(name, d):
+    """Heads shared through stride 0 pass through the same arithmetic as copies of them: equal bit for bit."""
+    import torch
+    import linear_kernelized_attention_b200 as F
+    q, k, v, do, g = _simple(2, 3, 200, d, name)
+    k1, v1 = k[:, :1].expand_as(q), v[:1, :1].expand_as(q)
+    got = (*F.favor_decay_attention(q, k1, v1, g, return_state=True), *F.favor_decay_attention_backward(q, k1, v1, g, do))
+    k2, v2 = k1.contiguous(), v1.contiguous()
+    ref = (*F.favor_decay_attention(q, k2, v2, g, return_state=True), *F.favor_decay_attention_backward(q, k2, v2, g, do))
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
