@@ -285,7 +285,8 @@ int favor_decode_step(const void* q, const void* k, const void* v, const void* o
  *   not overlap inputs; an output pointer equal to an input's returns FAVOR_ERR_UNSUPPORTED.
  * log_decay: device float [H], 4-byte aligned, natural logarithm of the decay: <= 0, -infinity
  *   (lambda = 0: each token by itself) included. A positive value grows the state instead, and is
- *   used as it is as long as exp(128 log_decay) is finite.
+ *   used as it is as long as exp(L log_decay) is a finite float: beyond it, weights overflow also of
+ *   tokens whose k is zero.
  * lengths: device int [B] or NULL (every sequence has L tokens): tokens of each sequence, held to
  *   [0, L]. Rows at and past the length are neither read into any result nor written. A sequence
  *   of no tokens has state_out = state_in.

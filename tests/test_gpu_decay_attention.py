@@ -630,3 +630,11 @@ def test_broadcast_head_is_its_copies(name, d):
     k2, v2 = k1.contiguous(), v1.contiguous()
     ref = (*F.favor_decay_attention(q, k2, v2, g, return_state=True), *F.favor_decay_attention_backward(q, k2, v2, g, do))
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("L,g", [(600, 0.1), (40, 2.0)])
+def test_growing_states_up_to_the_documented_limit(L, g, name):
+    """Positive log decays with exp(L g) within fp32, exp(128 g) beyond it for the short one."""
+    _forward_case(1, 1, L, 64, name, state=True, g=[g])
+    _backward_case(1, 1, L, 64, name, state=True, g=[g])
