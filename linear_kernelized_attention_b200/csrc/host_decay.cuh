@@ -111,8 +111,9 @@ int launch_scan(const dcy::Params& p, float* ws, int nseg, int seg, cudaStream_t
   const long long grid = (long long)p.B * p.H * p.nstates * ((p.d * p.d + dcy::kThreads - 1) / dcy::kThreads);
   if (grid > INT_MAX) return FAVOR_ERR_UNSUPPORTED;
   // 32 segments' loads in flight where there are many, 8 (a third of the registers, so more blocks an SM) where few.
-  // Measured, fp32 calls of d = 64, 8 against 32: one head of 1024 segments 191 and 166 us, 16 heads of 128 segments 162
-  // and 150; 16 heads of 16 segments 29.9 and 31.1, 256 heads of 2 segments 52 and 83.
+  // Measured, whole fp32 calls of d = 64 in us, 8 against 32. 16 heads: 16 segments 29.0 and 30.2, 32 46.1 and 47.5, 48
+  // 60.7 and 60.5, 64 79.6 and 77.9, 96 123 and 115, 128 161 and 150. One head: 32 segments 15.2 and 14.8, 64 18.8 and
+  // 18.0, 1024 201 and 165. 256 heads of 2 segments 52 and 83. Between 24 and 64 either does.
   return nseg >= 64 ? launch_with<dcy::ScanParams>(dcy::k_chunk_scan<32>, grid, dcy::kThreads, 0, st, true, sp)
                     : launch_with<dcy::ScanParams>(dcy::k_chunk_scan<8>, grid, dcy::kThreads, 0, st, true, sp);
 }
@@ -161,9 +162,16 @@ struct WalkPlan {
   bool scan;
 };
 
-// The number of segments with the least estimated time, in microseconds. Measured: a block of the walk takes
+// The number of segments with the least estimated time, in microseconds. The estimate: a block of the walk takes
 // 3 and 1.55 (d <= 64) or 2.95 a chunk, one of the states 3 and 1.0 or 2.2 a chunk, the scan and the gaps of
-// two further launches 7 and its traffic at 3 TB/s.
+// two further launches 7 and its traffic at 3 TB/s. The terms were fitted together, on whole calls with an earlier state
+// kernel; the present one takes 1.3 and 2.0 a chunk by itself. States that a caller wants back cost nothing more
+// with segments; without, their own pass over b and c, beside the walk, is not in the estimate.
+// Measured on the device, the pick against the best of 1 to 128 segments: prompts of 4 x 8 heads x 4096 tokens, d = 64,
+// 33.0 and 32.9; 16 x 65536 165 and 165; 65536 tokens of one head 31.4 and 31.4; 32 x 4096, d = 128, 62 and 62;
+// 8 x 8192, d = 128, 46.5 and 43.8; gradients 8 x 4096, d = 64, 27.7 and 27.7; 4 x 8 x 4096 47.2 and 47.2; 16 x 4096,
+// d = 128, 76 and 76. It misses on short prompts of few heads: 8 x 2048, d = 64, 16 segments 19.1 and 8 14.2; 2 x 8 x
+// 1024 with states, one segment 18.1 and 4 14.5.
 WalkPlan plan_walk(int BH, int L, int d, int nstates, int njobs) {
   const int nch = (int)(((long long)L + dtc::kTok - 1) / dtc::kTok), sms = sm_count();
   const double tw = d <= 64 ? 1.55 : 2.95, ts = d <= 64 ? 1.0 : 2.2;
@@ -314,9 +322,11 @@ int launch_decay_tc_t(const dcy::Params& p, const WalkPlan& pl, float* ws, cudaS
   }
   if (!sp.njobs) return launch_blocks(dtc::k_decay_walk<DP>, nwalk, WC::kThreads, WC::kSmem, false, tp, st);
   // The whole sequences' states: in the walk's own launch where the call is short (one block an SM, eight chunks
-  // at most), since the second launch costs the host 3 us (8 heads x 256 tokens of d = 64: 15.9 us in two launches, 14.5
-  // in one) but the joint kernel's registers slow a long walk (24 heads x 2049 tokens of d = 128: 61.5 us and 64.9);
-  // else beside it, or after it where they overwrite what it reads.
+  // at most), since a second launch costs about 3 us but the joint kernel has the walk's few registers a thread for the
+  // states too; else beside the walk, or after it where they overwrite what it reads. Measured on the device, two
+  // launches against one, prompts of 8 heads with states: d = 64, 1 chunk 11.0 and 7.9 us, 2 12.0 and 9.0, 4 13.9 and
+  // 11.7, 8 18.2 and 18.0, 12 22.6 and 24.2, 16 27.0 and 30.6; d = 128, 2 chunks 17.0 and 16.1, 8 30.4 and 29.7, 16
+  // 52.8 and 51.2. 74 heads of d = 128: 4 chunks 22.3 and 21.8, 8 32.1 and 33.0, 12 43.3 and 46.1.
   bool in_place = false;
   for (int i = 0; i < p.nstates; ++i) in_place = in_place || (p.s[i].out && p.s[i].out == p.s[i].in);
   if (!in_place && nwalk + nstate <= sm_count() && pl.cps <= 8) {

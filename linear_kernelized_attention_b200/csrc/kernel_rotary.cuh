@@ -7,9 +7,11 @@
 // The angle is reduced in double (t freq / pi, less the nearest even integer) before sin and cos of
 // an fp32 argument in [-1, 1] half turns: fp32 products of far positions lose the angle itself.
 //
-// Reading and writing q and k bounds it. One thread computes the sines of V pairs of one token once
-// and applies them to every head of its head group (q's heads, then k's), several heads' loads in
-// flight; heads are split into groups only where there are too few tokens to fill the GPU. Measured: 4 x 4096
+// Reading and writing q and k bounds it at best. One thread computes the sines of V pairs of one token once
+// and applies them to every head of its head group (q's heads, then k's), one after another: outputs may be the
+// inputs, so a head's loads stay behind the stores of the head before, and what is in flight comes from the number of
+// threads (its 55 registers hold one head's vectors, and of 14 warps a cycle issued 8 wait on loads). Heads
+// are split into groups only where there are too few tokens to fill the GPU. Measured: 4 x 4096
 // tokens of 8 + 8 heads of 64 columns in 13.7 us, 4900 GB/s (75% of a plain copy); twice as many groups, each
 // with the sines again, 15.9 us, and sines shared through shared memory 17.9 us.
 #pragma once
