@@ -157,9 +157,19 @@ cudaMemPool_t pool_for_device() {
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
-    if (cudaMemPoolCreate(&pools[dev], &props) != cudaSuccess) return nullptr;
+    // A process's first call may be one that is being captured. Making the pool is no part of the captured work, and a
+    // capture in its strictest mode would be invalidated by it.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    const cudaError_t made = cudaMemPoolCreate(&pools[dev], &props);
     uint64_t thr = UINT64_MAX;
-    cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &thr);
+    if (made == cudaSuccess) cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &thr);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (made != cudaSuccess) {
+      cudaGetLastError();
+      pools[dev] = nullptr;
+      return nullptr;
+    }
   }
   return pools[dev];
 }

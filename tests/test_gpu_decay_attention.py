@@ -638,3 +638,41 @@ def test_growing_states_up_to_the_documented_limit(L, g, name):
     """Positive log decays with exp(L g) within fp32, exp(128 g) beyond it for the short one."""
     _forward_case(1, 1, L, 64, name, state=True, g=[g])
     _backward_case(1, 1, L, 64, name, state=True, g=[g])
+
+
+FIRST_CALL = """
+import torch
+import linear_kernelized_attention_b200 as F
+q = (torch.randn(1, 2, 3000, 64, device="cuda") * 0.3).{dtype}()
+g = torch.full((2,), -0.05, device="cuda")
+out = torch.zeros_like(q)
+om = torch.randn(2, 64, 64, device="cuda").{dtype}()
+call = lambda: {call}
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call()
+graph.replay()
+torch.cuda.synchronize()
+got = out.clone()
+assert got.any()
+call()
+assert torch.equal(got, out) and F.favor_sync_status() == 0
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("dtype,call", [
+    ("bfloat16", "F.favor_decay_attention(q, q, q, g, out=out)"), ("float", "F.favor_decay_attention(q, q, q, g, out=out)"),
+    ("bfloat16", "F.favor_decay_attention_backward(q, q, q, g, q, dq=out)"),
+    ("bfloat16", "F.favor_attention(q, q, q, om, out=out)"),
+])
+def test_first_call_of_a_process_may_be_captured(dtype, call):
+    """The library's scratch pool is made on first use, also where that is inside a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(dtype=dtype, call=call)], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
