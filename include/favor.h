@@ -347,7 +347,7 @@ size_t favor_decay_workspace_bytes(int B, int H, int L, int d, int dtype_code, i
  * freq: device double [rot/2], radians per position (favor_rotary_frequencies). positions: device int
  * [B, L], or NULL for first_position + t. Angles are reduced in double, so far positions keep their
  * accuracy. k, k_out: NULL with Hk = 0. q_out may be q and k_out may be k with the same strides (in
- * place). strides: q, k, q_out, k_out (NULL = contiguous). Data pointers are aligned as
+ * place); other overlaps of an output with anything are not allowed. strides: q, k, q_out, k_out (NULL = contiguous). Data pointers are aligned as
  * favor_decay_attention's, freq to 8 bytes, positions to 4. Supported: rot even, 2 <= rot <= d <= 65536, Hq + Hk <= 65535.
  */
 int favor_rotary(const void* q, const void* k, const double* freq, const int* positions, void* q_out,
